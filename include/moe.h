@@ -326,6 +326,150 @@ moe_status moe_qk_norm_rope(int32_t T, int32_t n_q, int32_t n_kv, int32_t head_d
                             void* qkv, const int32_t* positions, int32_t max_pos, const void* q_norm_w,
                             const void* k_norm_w, const float* cos_sin, int32_t* bad_positions, void* stream);
 
+/* ---- Paged key/value cache: append, attention, compaction ------------------
+ * The attention-side steps between moe_qk_norm_rope and the expert layer of a
+ * serving step: new tokens' keys and values go into a paged cache, the new
+ * tokens attend to it (one token per sequence when decoding, a drafted chain or
+ * tree when speculating, a chunk when prefilling), and after a tree of drafts
+ * was verified the accepted nodes' keys and values move together.
+ *
+ * moe_kv_cache describes one layer's cache. Element (page p, kv head h, slot s,
+ * dimension i) of K and of V lies at p * page_stride + h * head_stride +
+ * s * slot_stride + i elements behind k and v, so [pages][heads][slots][d] and
+ * [pages][slots][heads][d] allocations, and K and V interleaved in one, all
+ * work.
+ *   k, v        device, 16-byte aligned; strides in elements, whole multiples of
+ *               16 bytes, at least head_dim, below 2^40 bytes (a stride over a
+ *               dimension of size 1 is not used)
+ *   page_size   slots per page: 16, 32, 64, 128 or 256
+ *   head_dim    64, 128 or 256
+ *   dtype       MOE_BF16, or MOE_E4M3: codes of value / scale, one scale for K
+ *               and one for V (finite, > 0; 1 for bf16 caches)
+ *
+ * moe_kv_batch describes the sequences of one call, all arrays on the device:
+ *   q_start     [B + 1] rows of sequence b are q_start[b] .. q_start[b+1] - 1 of
+ *               the call's T rows, in ascending order; rows outside every
+ *               sequence are padding and are left as they were
+ *   ctx_len     [B] tokens already in the cache; the sequence's new token i has
+ *               cache index ctx_len[b] + i
+ *   page_table  [B][max_pages]: cache index c lies in page page_table[b][c /
+ *               page_size], slot c % page_size. Entries behind a sequence's last
+ *               page are not read. Pages may be shared by sequences that only
+ *               read them; a page that a call writes to belongs to one sequence.
+ *   max_new     on the host: no sequence has more new rows than this
+ * B at most 4096, T at most 2^20. The arrays are read when the kernels run, so a
+ * captured graph replays with the lengths and pages of the time. Bad contents
+ * (rows outside [0, T), negative lengths, more tokens than the table holds, page
+ * ids outside [0, num_pages)) are never followed: the entry points say how each
+ * reports them. */
+typedef struct moe_kv_cache {
+    void* k;
+    void* v;
+    int64_t page_stride, head_stride, slot_stride;
+    int32_t num_pages, page_size, n_kv, head_dim, dtype;
+    float k_scale, v_scale;
+} moe_kv_cache;
+
+typedef struct moe_kv_batch {
+    const int32_t* q_start;
+    const int32_t* ctx_len;
+    const int32_t* page_table;
+    int32_t B, max_pages, max_new;
+} moe_kv_batch;
+
+/* moe_qk_norm_rope with the cache append in the same pass: of every new token
+ * the q heads are normalised, rotated and written to q_out, the k heads the same
+ * and written to the cache, the v heads written to the cache. fp32 arithmetic,
+ * one rounding (to bf16, or to E4M3_rn_satfinite(value / scale)); the q rows and
+ * bf16 keys are those of moe_qk_norm_rope bit for bit.
+ *   qkv        [T] rows of (n_q + 2*n_kv) * head_dim bf16, qkv_stride elements
+ *              apart (q heads | k heads | v heads); not changed
+ *   positions  [T] int32 rotation positions, each in [0, max_pos); drafted tree
+ *              nodes at equal depth share one (unused and may be NULL when
+ *              rot_dim == 0, as may cos_sin)
+ *   q_norm_w, k_norm_w  [head_dim] bf16, or NULL: no norm for those heads
+ *   q_out      [T] rows of n_q * head_dim bf16, q_stride elements apart; may be
+ *              qkv itself with the same stride (in place)
+ *   bad_tokens device int32 counter or NULL: one is added per token that has a
+ *              position out of range (nothing of it is written) or no usable
+ *              cache slot (only its q row is written)
+ * head_dim and rot_dim as in moe_qk_norm_rope; both row strides multiples of 8,
+ * pointers 16-byte aligned. No workspace. */
+moe_status moe_qk_norm_rope_append(const moe_kv_cache* cache, const moe_kv_batch* batch, int32_t T, int32_t n_q,
+                                   int32_t rot_dim, float eps, const void* qkv, int64_t qkv_stride,
+                                   const int32_t* positions, int32_t max_pos, const void* q_norm_w,
+                                   const void* k_norm_w, const float* cos_sin, void* q_out, int64_t q_stride,
+                                   int32_t* bad_tokens, void* stream);
+
+/* Attention of the new tokens over the cache, which already holds their keys and
+ * values (moe_qk_norm_rope_append). Query head h reads kv head h / (n_q / n_kv).
+ * Row i of sequence b sees every cached token (index < ctx_len[b]) and, of the
+ * sequence's own new tokens, those that tree_mask names:
+ *   tree_mask  [T][mask_words] uint64: bit j % 64 of word j / 64 of a row says
+ *              whether the row sees new token j of its sequence (a tree node
+ *              names its ancestors and itself). NULL (mask_words 0): a chain, row
+ *              i sees the new tokens 0..i, which is decoding, a drafted chain or
+ *              a prefill chunk. With a mask max_new <= 64 * mask_words,
+ *              mask_words <= 64.
+ *   out[t][h] = sum_j p_j v_j,  p = softmax_j(softmax_scale * q . k_j), in fp32
+ *              (p is rounded to the matrix instructions' 16-bit operands in the
+ *              product with v), rounded once to bf16
+ *   lse[t][h] = ln sum_j exp(softmax_scale * q . k_j), fp32, or lse NULL
+ * A row that sees nothing (or only scores of -infinity) gives zeros and -infinity.
+ * Keys and values that a row does not see do not reach it, whatever they hold.
+ *   q    [T] rows of n_q * head_dim bf16, q_stride elements apart
+ *   out  the same with out_stride; lse [T][n_q]
+ *   ws   moe_tree_attention_workspace_size bytes, 256-byte aligned, zeroed once
+ *        by the caller before the first use; bad contents of the batch's arrays
+ *        leave MOE_ERR_DEVICE in its status word (moe_get_status): the rows of a
+ *        sequence with bad lengths are left as they were, a block of keys with a
+ *        bad page id counts as not seen
+ * n_q a multiple of n_kv, n_q <= 1024; row strides multiples of 8; softmax_scale
+ * finite. The result does not depend on the timing of the run (no atomics in the
+ * sums), but a row's rounding may depend on the other sequences of the batch. */
+moe_status moe_tree_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, int32_t T, int32_t n_q,
+                              float softmax_scale, const void* q, int64_t q_stride, const uint64_t* tree_mask,
+                              int32_t mask_words, void* out, int64_t out_stride, float* lse, void* ws,
+                              size_t ws_bytes, void* stream);
+/* Bytes of workspace for calls with this cache and at most T rows; 0 if invalid. */
+size_t moe_tree_attention_workspace_size(const moe_kv_cache* cache, int32_t n_q, int32_t T);
+
+/* After verifying drafts: for each sequence the keys and values of its accepted
+ * new tokens move to the front of its new tokens, cache index ctx_len[b] +
+ * accepted[b][i] to ctx_len[b] + i, in n_layers layers at once (layer l's cache
+ * lies l * layer_stride elements behind `cache`; unused for one layer). The
+ * caller then adds n_accepted[b] to ctx_len[b].
+ *   accepted    [B][max_accept] int32, each row's first n_accepted[b] entries
+ *               strictly ascending, in [0, new tokens of b) (so sources never lie
+ *               in front of their destinations and the move is done in place)
+ *   n_accepted  [B] int32 in [0, max_accept]
+ *   bad_seqs    device int32 counter or NULL: one is added per sequence whose
+ *               lists or lengths are not so, or which reaches a bad page id; of
+ *               such a sequence nothing moves
+ * max_accept 1..1024, n_layers 1..4096. No workspace. */
+moe_status moe_kv_compact(const moe_kv_cache* cache, const moe_kv_batch* batch, int32_t n_layers,
+                          int64_t layer_stride, const int32_t* accepted, int32_t max_accept,
+                          const int32_t* n_accepted, int32_t* bad_seqs, void* stream);
+
+/* Log probabilities of given tokens under rows of logits, with the entropy and
+ * the likeliest alternatives of each row:
+ *   logprobs[t]        = x_t[targets[t]] - ln sum_v exp(x_t[v])
+ *   entropy[t]         = -sum_v p_v ln p_v,  p = softmax(x_t)        (or NULL)
+ *   top_ids[t][i]      the i-th largest logit's id, ties to the lower id,
+ *   top_logprobs[t][i] its log probability                (both NULL if top_n = 0)
+ * One pass over the logits; fp32 sums that leave out the largest term, so that
+ * rows with one likely token keep their relative accuracy.
+ *   logits  [T] rows of V values, dtype MOE_BF16 or MOE_F32, row_stride >= V
+ *           elements apart; any alignment of the type
+ *   targets [T] int32, or NULL with logprobs NULL; a target outside [0, V) gives NaN
+ * -infinity is a probability of 0. A row that holds NaN or +infinity, or nothing
+ * but -infinity, gives NaN for every log probability and the entropy (in top_ids
+ * NaN ranks above +infinity). T at most 2^20, V at most 2^24, top_n at most 32
+ * and V. No workspace. */
+moe_status moe_token_logprobs(int32_t T, int32_t V, int32_t dtype, const void* logits, int64_t row_stride,
+                              const int32_t* targets, int32_t top_n, float* logprobs, float* entropy,
+                              int32_t* top_ids, float* top_logprobs, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,7 +24,8 @@ EXPORTS = ("moe_workspace_size", "moe_route_topk", "moe_permute", "moe_grouped_f
            "moe_clear_status", "moe_status_string", "moe_launch_count", "moe_profile_enable",
            "moe_profile_reset", "moe_profile_read", "moe_inject_wait_timeout",
            "moe_permute_noalloc", "moe_qk_norm_rope", "moe_cast_f32_bf16", "moe_inject_fold_timeout",
-           "moe_inject_route_timeout")
+           "moe_inject_route_timeout", "moe_qk_norm_rope_append", "moe_tree_attention",
+           "moe_tree_attention_workspace_size", "moe_kv_compact", "moe_token_logprobs")
 
 
 class MoeError(RuntimeError):
@@ -38,6 +39,17 @@ class moe_shape(C.Structure):
                 ("top_k", C.c_int32), ("shared_id", C.c_int32), ("shared_weight", C.c_float),
                 ("renormalize", C.c_int32), ("act_dtype", C.c_int32), ("w_dtype", C.c_int32),
                 ("routed_scale", C.c_float), ("bias_select_only", C.c_int32), ("out_f32", C.c_int32)]
+
+
+class moe_kv_cache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64), ("head_stride", C.c_int64),
+                ("slot_stride", C.c_int64), ("num_pages", C.c_int32), ("page_size", C.c_int32), ("n_kv", C.c_int32),
+                ("head_dim", C.c_int32), ("dtype", C.c_int32), ("k_scale", C.c_float), ("v_scale", C.c_float)]
+
+
+class moe_kv_batch(C.Structure):
+    _fields_ = [("q_start", C.c_void_p), ("ctx_len", C.c_void_p), ("page_table", C.c_void_p), ("B", C.c_int32),
+                ("max_pages", C.c_int32), ("max_new", C.c_int32)]
 
 
 _lib = None
@@ -91,6 +103,17 @@ def lib() -> C.CDLL:
         L.moe_cast_f32_bf16.argtypes = [sz, p, p, p]
         L.moe_qk_norm_rope.restype = i
         L.moe_qk_norm_rope.argtypes = [i, i, i, i, i, f, p, p, i, p, p, p, p, p]
+        i64, KC, KB = C.c_int64, C.POINTER(moe_kv_cache), C.POINTER(moe_kv_batch)
+        L.moe_qk_norm_rope_append.restype = i
+        L.moe_qk_norm_rope_append.argtypes = [KC, KB, i, i, i, f, p, i64, p, i, p, p, p, p, i64, p, p]
+        L.moe_tree_attention_workspace_size.restype = sz
+        L.moe_tree_attention_workspace_size.argtypes = [KC, i, i]
+        L.moe_tree_attention.restype = i
+        L.moe_tree_attention.argtypes = [KC, KB, i, i, f, p, i64, p, i, p, i64, p, p, sz, p]
+        L.moe_kv_compact.restype = i
+        L.moe_kv_compact.argtypes = [KC, KB, i, i64, p, i, p, p, p]
+        L.moe_token_logprobs.restype = i
+        L.moe_token_logprobs.argtypes = [i, i, i, p, i64, p, i, p, p, p, p, p]
         _lib = L
     return _lib
 
@@ -197,6 +220,170 @@ def moe_cast_f32_bf16(inp, out, stream=None):
 def moe_quant_rows_e4m3(rows, cols, inp, codes, scales, stream=None):
     _check("moe_quant_rows_e4m3", lib().moe_quant_rows_e4m3(
         rows, cols, _p(inp), _p(codes), _p(scales), _stream(stream)))
+
+
+# ---- paged cache, tree attention, log probabilities
+
+def _rows(name, t, dtype):
+    """Row stride of a tensor whose rows are dense: [T, n] or [T, heads, d]."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    inner = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != inner:
+            raise ValueError(f"{name}: the rows of a [T, ...] tensor have to be dense")
+        inner *= size
+    return t.stride(0) if t.shape[0] > 1 else max(inner, t.stride(0))
+
+
+def _dense(name, t, dtype, shape=None):
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} has to be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
+
+
+def make_kv_cache(k, v, k_scale: float = 1.0, v_scale: float = 1.0) -> moe_kv_cache:
+    """moe_kv_cache of K and V tensors [pages, kv heads, page size, head dim] (views of
+    any layout with dense head rows, the same for both): bf16, or uint8 / float8_e4m3fn
+    for E4M3 codes of value / scale. It keeps the tensors alive."""
+    if k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.device != v.device or k.dim() != 4:
+        raise ValueError("k and v: [pages, kv heads, page size, head dim], alike in type, strides and device")
+    if k.stride(3) != 1:
+        raise ValueError("the head dimension has to be dense")
+    dt = {torch.bfloat16: MOE_BF16, torch.uint8: MOE_E4M3, torch.float8_e4m3fn: MOE_E4M3}.get(k.dtype)
+    if dt is None:
+        raise TypeError(f"a cache of {k.dtype}")
+    c = moe_kv_cache(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), k.shape[0], k.shape[2],
+                     k.shape[1], k.shape[3], dt, k_scale, v_scale)
+    c.tensors = (k, v)
+    return c
+
+
+def make_kv_batch(q_start, ctx_len, page_table, max_new: int) -> moe_kv_batch:
+    """moe_kv_batch of int32 device tensors q_start [B + 1], ctx_len [B], page_table
+    [B, max_pages]; it keeps them alive, and calls read what they hold at the time."""
+    B = ctx_len.shape[0]
+    _dense("q_start", q_start, torch.int32, (B + 1,))
+    _dense("ctx_len", ctx_len, torch.int32, (B,))
+    _dense("page_table", page_table, torch.int32, (B, page_table.shape[1]))
+    b = moe_kv_batch(q_start.data_ptr(), ctx_len.data_ptr(), page_table.data_ptr(), B, page_table.shape[1], max_new)
+    b.tensors = (q_start, ctx_len, page_table)
+    return b
+
+
+class _on:
+    """The device of `t` made current for a launch (streams belong to a device)."""
+
+    def __init__(self, t):
+        at = t.device.index
+        self.guard = None if at is None or at == torch.cuda.current_device() else torch.cuda.device(at)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def moe_qk_norm_rope_append(cache, batch, n_q: int, rot: int, eps: float, qkv, positions, q_norm_w, k_norm_w, cos_sin,
+                            q_out, bad_tokens=None, stream=None):
+    """qkv [T, (n_q + 2 n_kv) d] bf16 -> q_out [T, n_q d] bf16 and the cache (see
+    include/moe.h); q_norm_w / k_norm_w None: no norm, rot 0: no rotation."""
+    d, T = cache.head_dim, qkv.shape[0]
+    qs, os_ = _rows("qkv", qkv, torch.bfloat16), _rows("q_out", q_out, torch.bfloat16)
+    if qkv[:1].numel() not in (0, (n_q + 2 * cache.n_kv) * d) or q_out.shape[0] != T or \
+            q_out[:1].numel() not in (0, n_q * d, (n_q + 2 * cache.n_kv) * d):
+        raise ValueError("qkv [T, (n_q + 2 n_kv) d] and q_out [T, n_q d]")
+    _dense("q_norm_w", q_norm_w, torch.bfloat16, (d,))
+    _dense("k_norm_w", k_norm_w, torch.bfloat16, (d,))
+    _dense("bad_tokens", bad_tokens, torch.int32)
+    max_pos = 0
+    if rot > 0:
+        _dense("positions", positions, torch.int32, (T,))
+        _dense("cos_sin", cos_sin, torch.float32, (cos_sin.shape[0], rot))
+        max_pos = cos_sin.shape[0]
+    with _on(qkv):
+        _check("moe_qk_norm_rope_append", lib().moe_qk_norm_rope_append(
+            C.byref(cache), C.byref(batch), T, n_q, rot, eps, _p(qkv), qs, _p(positions if rot > 0 else None), max_pos,
+            _p(q_norm_w), _p(k_norm_w), _p(cos_sin if rot > 0 else None), _p(q_out), os_, _p(bad_tokens),
+            _stream(stream)))
+
+
+def moe_tree_attention_workspace_size(cache, n_q: int, T: int) -> int:
+    n = lib().moe_tree_attention_workspace_size(C.byref(cache), n_q, T)
+    if n == 0:
+        raise MoeError("moe_tree_attention_workspace_size", MOE_ERR_INVALID_ARG)
+    return n
+
+
+def alloc_tree_attention_workspace(cache, n_q: int, T: int, device=None) -> torch.Tensor:
+    """Zeroed workspace of moe_tree_attention for at most T rows over this cache."""
+    n = moe_tree_attention_workspace_size(cache, n_q, T)
+    ws = torch.zeros(n + 256, dtype=torch.uint8, device=cache.tensors[0].device if device is None else device)
+    off = (-ws.data_ptr()) % 256
+    return ws[off:off + n]
+
+
+def moe_tree_attention(cache, batch, n_q: int, q, out, ws, tree_mask=None, lse=None, scale: float | None = None,
+                       stream=None):
+    """q [T, n_q d] bf16 over the cache -> out [T, n_q d] bf16, lse [T, n_q] fp32 or None;
+    tree_mask [T, words] int64 (bit j: the row sees its sequence's new token j) or None
+    for a chain; scale None: 1 / sqrt(head dim)."""
+    T, d = q.shape[0], cache.head_dim
+    qs, os_ = _rows("q", q, torch.bfloat16), _rows("out", out, torch.bfloat16)
+    if out.shape[0] != T or q[:1].numel() not in (0, n_q * d) or out[:1].numel() not in (0, n_q * d):
+        raise ValueError("q and out: [T, n_q d]")
+    _dense("lse", lse, torch.float32, (T, n_q))
+    words = 0
+    if tree_mask is not None:
+        words = tree_mask.shape[1]
+        _dense("tree_mask", tree_mask, torch.int64, (T, words))
+    with _on(q):
+        _check("moe_tree_attention", lib().moe_tree_attention(
+            C.byref(cache), C.byref(batch), T, n_q, d ** -0.5 if scale is None else scale, _p(q), qs, _p(tree_mask), words,
+            _p(out), os_, _p(lse), _p(ws), ws.numel(), _stream(stream)))
+
+
+def moe_kv_compact(cache, batch, accepted, n_accepted, n_layers: int = 1, layer_stride: int = 0, bad_seqs=None,
+                   stream=None):
+    """Moves accepted [B, max_accept] int32 new tokens' keys and values to the front of
+    their sequences' new tokens, in place, in n_layers caches layer_stride elements apart."""
+    B = batch.B
+    _dense("accepted", accepted, torch.int32, (B, accepted.shape[1]))
+    _dense("n_accepted", n_accepted, torch.int32, (B,))
+    _dense("bad_seqs", bad_seqs, torch.int32)
+    with _on(accepted):
+        _check("moe_kv_compact", lib().moe_kv_compact(
+            C.byref(cache), C.byref(batch), n_layers, layer_stride, _p(accepted), accepted.shape[1], _p(n_accepted),
+            _p(bad_seqs), _stream(stream)))
+
+
+def moe_token_logprobs(logits, targets, logprobs, entropy=None, top_ids=None, top_logprobs=None, stream=None):
+    """logits [T, V] (bf16 or fp32, dense rows) and targets [T] int32 -> logprobs [T],
+    entropy [T], top_ids / top_logprobs [T, n], each fp32 (ids int32) or None."""
+    T, V = logits.shape
+    dt = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}.get(logits.dtype)
+    if dt is None:
+        raise TypeError(f"logits are {logits.dtype}, not bf16 or fp32")
+    _dense("targets", targets, torch.int32, (T,))
+    _dense("logprobs", logprobs, torch.float32, (T,))
+    _dense("entropy", entropy, torch.float32, (T,))
+    n = 0
+    if top_ids is not None:
+        n = top_ids.shape[1]
+        _dense("top_ids", top_ids, torch.int32, (T, n))
+        _dense("top_logprobs", top_logprobs, torch.float32, (T, n))
+    with _on(logits):
+        _check("moe_token_logprobs", lib().moe_token_logprobs(
+            T, V, dt, _p(logits), _rows("logits", logits, logits.dtype), _p(targets), n, _p(logprobs), _p(entropy),
+            _p(top_ids if n else None), _p(top_logprobs if n else None), _stream(stream)))
 
 
 def moe_get_status(ws, stream=None) -> int:
