@@ -126,7 +126,8 @@ moe_status moe_qk_norm_rope_append(const moe_kv_cache* cache, const moe_kv_batch
 size_t moe_tree_attention_workspace_size(const moe_kv_cache* cache, int32_t n_q, int32_t T) {
     if (check_cache(cache) != MOE_OK || check_heads(*cache, n_q) != MOE_OK || T < 0 || T > kMaxT) return 0;
     // partial results of the items that a cut between two blocks' shares goes through
-    return sizeof(DevStatus) + static_cast<size_t>(2) * kSmallBlocks * kSmallRows * (2 + cache->head_dim) * sizeof(float);
+    const size_t rows = kTileBlocks * kTileRows > kSmallBlocks * kSmallRows ? kTileBlocks * kTileRows : kSmallBlocks * kSmallRows;
+    return sizeof(DevStatus) + 2 * rows * (2 + cache->head_dim) * sizeof(float);
 }
 
 moe_status moe_tree_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, int32_t T, int32_t n_q,
@@ -165,7 +166,10 @@ moe_status moe_tree_attention(const moe_kv_cache* cache, const moe_kv_batch* bat
     a.out_stride = out_stride;
     a.lse = lse;
     a.status = static_cast<DevStatus*>(ws);
-    return from_cuda(launch_tree_attn_small(a, static_cast<char*>(ws) + sizeof(DevStatus), static_cast<cudaStream_t>(stream)));
+    void* partials = static_cast<char*>(ws) + sizeof(DevStatus);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return from_cuda(tree_attn_tiles_apply(a) ? launch_tree_attn_tiles(a, partials, st)
+                                              : launch_tree_attn_small(a, partials, st));
 }
 
 moe_status moe_kv_compact(const moe_kv_cache* cache, const moe_kv_batch* batch, int32_t n_layers,

@@ -90,7 +90,8 @@ EncodeTiledFn encode_tiled() {
 
 // K or V of a cache as (dimension within a 128-byte span, slot, span, kv head, page): a box
 // of all spans of box_rows slots of one head lands as [span][slot][128 bytes], swizzled.
-bool make_kv_map(CUtensorMap* m, const AttnArgs& a, bool v, int box_rows) {
+// With all_spans false a box is one span.
+bool make_kv_map(CUtensorMap* m, const AttnArgs& a, bool v, int box_rows, bool all_spans) {
     EncodeTiledFn fn = encode_tiled();
     if (fn == nullptr) return false;
     const int esz = a.f8 ? 1 : 2;
@@ -103,7 +104,7 @@ bool make_kv_map(CUtensorMap* m, const AttnArgs& a, bool v, int box_rows) {
     const cuuint64_t strides[4] = {slot, static_cast<cuuint64_t>(span), a.c.n_kv > 1 ? static_cast<cuuint64_t>(a.c.head_b) : slot,
                                    a.c.num_pages > 1 ? static_cast<cuuint64_t>(a.c.page_b) : slot};
     const cuuint32_t box[5] = {static_cast<cuuint32_t>(span / esz), static_cast<cuuint32_t>(box_rows),
-                               static_cast<cuuint32_t>(a.head_dim * esz / span), 1, 1};
+                               all_spans ? static_cast<cuuint32_t>(a.head_dim * esz / span) : 1u, 1, 1};
     const cuuint32_t es[5] = {1, 1, 1, 1, 1};
     return fn(m, a.f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, v ? a.c.v : a.c.k, dims, strides,
               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,

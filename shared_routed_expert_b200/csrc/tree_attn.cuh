@@ -258,9 +258,13 @@ struct Partials {
 
 constexpr int kSmallBlocks = 320;        // most blocks of the 16- to 64-row kernel
 constexpr int kSmallRows = 64;
+constexpr int kTileBlocks = 160;         // most blocks of the 256-row kernel
+constexpr int kTileRows = 256;
 
 cudaError_t launch_tree_attn_small(const AttnArgs& a, void* partials, cudaStream_t st);
 cudaError_t launch_tree_attn_join(const AttnArgs& a, Tiling g, Partials p, int blocks, int least, cudaStream_t st);
-bool make_kv_map(CUtensorMap* m, const AttnArgs& a, bool v, int box_rows);
+bool make_kv_map(CUtensorMap* m, const AttnArgs& a, bool v, int box_rows, bool all_spans);
+bool tree_attn_tiles_apply(const AttnArgs& a);
+cudaError_t launch_tree_attn_tiles(const AttnArgs& a, void* partials, cudaStream_t st);
 
 }  // namespace sre

@@ -556,7 +556,7 @@ cudaError_t launch_cfg(const AttnArgs& a, void* partials, int sms, cudaStream_t 
     p.box_shift = page < CK ? a.c.page_shift : 5;
     p.least = 2;
     p.wait_limit = 4ll << 30;
-    if (!make_kv_map(&p.tk, a, false, box) || !make_kv_map(&p.tv, a, true, box)) return cudaErrorInvalidValue;
+    if (!make_kv_map(&p.tk, a, false, box, true) || !make_kv_map(&p.tv, a, true, box, true)) return cudaErrorInvalidValue;
     const int blocks = sms * S::BLOCKS_PER_SM < kSmallBlocks ? sms * S::BLOCKS_PER_SM : kSmallBlocks;
     p.part.ml = static_cast<float*>(partials);
     p.part.o = p.part.ml + static_cast<size_t>(2) * kSmallBlocks * kSmallRows * 2;

@@ -1,0 +1,535 @@
+// Attention over a paged cache for many query rows per kv head (prefill chunks, larger
+// trees): bound by the tensor cores and the exponentials.
+//
+// A block takes tiles of 256 packed query rows as two halves of 128 that take turns on the
+// tensor cores, and runs along its share of the key axis (tree_attn.cuh) in steps of 128 keys:
+//   S_h = Q_h K^T         tcgen05.mma, Q and K in shared memory, S in TMEM (fp32)
+//   P_h = 2^(S_h - m)     four warps per half, one thread per row; P (bf16) overwrites S in TMEM
+//   O_h += P_h V          tcgen05.mma with P read from TMEM, V in shared memory (keys as K,
+//                         so V is used as it is stored, MN-major), O in TMEM (fp32)
+// While one half's exponentials run, the other half's products do. The running maximum is
+// raised (and O rescaled, in TMEM) only when a row's grows by more than 2^8, so that
+// rescaling is rare; sums and statistics are fp32, P is rounded to bf16 for the product.
+// Roles: warps 0-3 and 4-7 the two halves' softmax, loads of Q and epilogue; warp 8 issues
+// the products; warp 9 streams K and V boxes (one per page piece and 128-byte span) through
+// a ring in shared memory. Every wait is bounded.
+#include "kernels.cuh"
+#include "tc_ptx.cuh"
+#include "tree_attn.cuh"
+
+namespace sre {
+
+namespace {
+
+constexpr int TK = 128;                  // keys per step
+constexpr int TL_THREADS = 320;
+constexpr int kInfo = 8;                 // steps whose key masks are kept (the producer is at most 6 ahead)
+
+template <int D>
+struct Tile {
+    static constexpr int SPANS = D * 2 / 128;
+    static constexpr int SPAN = 128 * 128;                         // bytes of a span of 128 rows
+    static constexpr int QHALF = SPANS * SPAN;
+    static constexpr int SLOT = SPANS * SPAN;                      // K or V of a step
+    static constexpr int NS = D == 128 ? 5 : 10;
+    static constexpr int SMEM = 2 * QHALF + NS * SLOT + 1024;
+};
+
+struct TileParams {
+    AttnArgs a;
+    CUtensorMap tk, tv;
+    Partials part;
+    int box_shift;
+    int least;
+    long long wait_limit;
+};
+
+__device__ __forceinline__ float tl_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A row of an item again, key by key (a rare path, kept out of the main code's registers)
+template <int D>
+__device__ __noinline__ void redo_row(const AttnArgs& a, const Cursor& c, int i, int head, int lo, int hi, float* o, float* ml,
+                                      int lane) {
+    constexpr int EPL = D / 32;
+    float q[EPL], acc[EPL], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        q[j] = bf16_to_f32(a.q[(c.s.row0 + i) * a.q_stride + head * D + lane * EPL + j]);
+        acc[j] = 0.f;
+    }
+    attend_row<EPL, false>(a, c.b, c.s, i, c.h, q, lo, hi, m, l, acc, lane);
+    if (o != nullptr) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) o[lane * EPL + j] = acc[j];
+        if (lane == 0) {
+            ml[0] = m;
+            ml[1] = l;
+        }
+    } else {
+        const long long row = c.s.row0 + i;
+        const float inv = l == 0.f ? 0.f : a.c.v_scale / l;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            a.out[row * a.out_stride + head * D + lane * EPL + j] = f32_to_bf16(l == 0.f ? 0.f : acc[j] * inv);
+        if (a.lse != nullptr && lane == 0) a.lse[row * a.n_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2F;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_constant__ TileParams p) {
+    using S = Tile<D>;
+    constexpr int NS = S::NS;
+    constexpr Tiling G{kTileRows, TK};
+    extern __shared__ __align__(1024) unsigned char tl_raw[];
+    __shared__ ScanShared scan;
+    __shared__ uint64_t full[NS], empty[NS], q_ready[2], s_full[2], p_ready[2], o_full[2], tail_bar, drain_bar;
+    __shared__ uint32_t info[kInfo][4];  // keys of a step that were loaded
+    __shared__ uint32_t tmem_base_s;
+    __shared__ int s_abort;
+    unsigned char* smem = tl_raw + ((1024 - (ptx::smem_u32(tl_raw) & 1023)) & 1023);
+    unsigned char* ring = smem + 2 * S::QHALF;
+    volatile int* abort_flag = &s_abort;
+    const AttnArgs& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int i = 0; i < NS; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], 1);
+        }
+        for (int h = 0; h < 2; ++h) {
+            ptx::mbar_init(&q_ready[h], 128);
+            ptx::mbar_init(&s_full[h], 1);
+            ptx::mbar_init(&p_ready[h], 128);
+            ptx::mbar_init(&o_full[h], 1);
+        }
+        ptx::mbar_init(&tail_bar, 1);
+        ptx::mbar_init(&drain_bar, 1);
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&p.tk);
+        ptx::prefetch_tmap(&p.tv);
+    }
+    long long before;
+    int b0, b1;
+    const long long W = scan_steps(a, G, scan, &before, &b0, &b1);
+    const int shares = W > 0 ? share_count(W, gridDim.x, p.least) : 0;
+    if (static_cast<int>(blockIdx.x) >= shares) return;
+    const long long x0 = share_begin(W, blockIdx.x, shares), x1 = share_begin(W, blockIdx.x + 1, shares);
+    Cursor cur = seek(a, G, scan, x0, before, b0, b1);
+    long long left = x1 - x0;
+    if (warp == 8) {
+        ptx::tmem_alloc(&tmem_base_s, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = tmem_base_s;   // columns: S0 0, S1 128, O0 256, O1 384
+
+    if (warp == 9) {
+        // ------------------------------------------------------------ producer
+        const int box = 1 << p.box_shift, pieces = TK >> p.box_shift;
+        uint32_t n = 0, step_no = 0, tail_phase = 0;               // slots and steps so far
+        bool ok = true;
+        while (left > 0 && ok) {
+            const int lo = cur.step, hi = static_cast<int>(min(static_cast<long long>(cur.steps), lo + left));
+            const int keys = tile_keys(a, cur.s, cur.mt, G.M);
+            const int32_t* table = a.c.page_table + static_cast<size_t>(cur.b) * a.c.max_pages;
+            const int first = lo * TK, stop = min(hi * TK, keys);
+            auto fetch = [&](int piece) {
+                const int c = first + ((piece + lane) << p.box_shift);
+                return c < stop ? table[c >> a.c.page_shift] : -1;
+            };
+            int base = 0;
+            int page_now = fetch(0), page_next = fetch(32);
+            for (int st = lo; st < hi && ok; ++st, ++step_no) {
+                const int c0 = st * TK;
+                const int at = (c0 - first) >> p.box_shift;
+                if (at - base >= 32) {                             // (pieces per step divide 32)
+                    base += 32;
+                    page_now = page_next;
+                    page_next = fetch(base + 32);
+                }
+                // lane q < pieces: piece q of this step
+                const int page = __shfl_sync(0xFFFFFFFFu, page_now, (at - base + lane) & 31);
+                const int c = c0 + (lane << p.box_shift);
+                const bool wanted = lane < pieces && c < keys;
+                const bool good = wanted && page >= 0 && page < a.c.num_pages;
+                if (wanted && !good) report(a.status, MOE_ERR_DEVICE, cur.b);
+                const uint32_t goods = __ballot_sync(0xFFFFFFFFu, good);
+                uint32_t word = 0xFFFFFFFFu;                       // lane q < 4: keys 32 q .. of the step
+                {
+                    const int k0 = lane * 32, rest = keys - (c0 + k0);
+                    if (rest < 32) word = rest <= 0 ? 0u : (1u << rest) - 1u;
+                    if (box >= 32) {
+                        if (!(goods >> ((k0 >> p.box_shift) & 31) & 1)) word = 0;
+                    } else {
+                        if (!(goods >> ((2 * lane) & 31) & 1)) word &= 0xFFFF0000u;
+                        if (!(goods >> ((2 * lane + 1) & 31) & 1)) word &= 0xFFFFu;
+                    }
+                }
+                if (lane < 4) info[step_no % kInfo][lane] = word;
+                __syncwarp();
+                const bool partial = __any_sync(0xFFFFFFFFu, lane < 4 && word != 0xFFFFFFFFu);
+                const uint32_t bytes = static_cast<uint32_t>(__popc(goods)) * box * 128u * S::SPANS;
+                const int slot_in_page = c & ((1 << a.c.page_shift) - 1);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const uint32_t sl = n % NS;
+                    ok = ok && ptx::mbar_wait(&empty[sl], ((n / NS) & 1u) ^ 1u, abort_flag, p.wait_limit, a.status, 1u);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    const bool tail = kv == 1 && partial;
+                    uint64_t* bar = tail ? &tail_bar : &full[sl];
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
+                    __syncwarp();
+                    unsigned char* dst = ring + sl * S::SLOT;
+                    if (good) {
+#pragma unroll
+                        for (int sp = 0; sp < S::SPANS; ++sp)
+                            ptx::tma_load_5d(dst + sp * S::SPAN + lane * box * 128, kv ? &p.tv : &p.tk, bar, 0, slot_in_page,
+                                             sp, cur.h, page);
+                    }
+                    if (tail) {
+                        // keys that are not there count as zero, not as 0 * whatever lies there
+                        ok = ptx::mbar_wait(&tail_bar, tail_phase, abort_flag, p.wait_limit, a.status, 7u);
+                        tail_phase ^= 1u;
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        for (int r = lane; r < TK; r += 32) {
+                            const uint32_t w = __shfl_sync(0xFFFFFFFFu, word, r >> 5);
+                            if (w >> (r & 31) & 1) continue;
+                            for (int sp = 0; sp < S::SPANS; ++sp)
+#pragma unroll
+                                for (int ch = 0; ch < 8; ++ch)
+                                    *reinterpret_cast<uint4*>(dst + sp * S::SPAN + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&full[sl]);
+                    }
+                }
+            }
+            left -= hi - lo;
+            if (left > 0) cur.next(a, G);
+        }
+        if (lane == 0 && *abort_flag) {
+            // every copy in flight lands before the block's memory goes away
+            for (uint32_t i = 0; i < NS; ++i) {
+                const uint32_t uses = n > i ? (n - i + NS - 1) / NS : 0;   // times slot i was armed
+                if (uses == 0) continue;
+                const long long t0 = clock64();
+                while (!ptx::mbar_try_wait(&full[i], (uses - 1) & 1u) && clock64() - t0 < p.wait_limit) {
+                }
+            }
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ products
+        if (lane == 0) {
+            constexpr uint32_t IS = ptx::instr_desc(128, TK, 1);
+            constexpr uint32_t IO = ptx::instr_desc(128, D, 1) | ptx::kBMnMajor;
+            const uint32_t q_u = ptx::smem_u32(smem), ring_u = ptx::smem_u32(ring);
+            uint32_t n = 0, qp[2] = {0, 0}, pp[2] = {0, 0};
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t par, unsigned site) {
+                ok = ok && ptx::mbar_wait(bar, par, abort_flag, p.wait_limit, a.status, site);
+                return ok;
+            };
+            auto scores = [&](int h, uint32_t kslot) {
+                const uint32_t ka = ring_u + kslot * S::SLOT, qa = q_u + h * S::QHALF;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k >> 2) * S::SPAN + (k & 3) * 32;
+                    ptx::mma_f16(tmem + h * 128, ptx::smem_desc_sw<128>(qa + off), ptx::smem_desc_sw<128>(ka + off), IS, k != 0);
+                }
+            };
+            auto values = [&](int h, uint32_t vslot, bool add) {
+                const uint32_t va = ring_u + vslot * S::SLOT;
+#pragma unroll
+                for (int k = 0; k < TK / 16; ++k)
+                    ptx::mma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8, ptx::smem_desc_mn128(va + k * 2048, S::SPAN), IO,
+                                    add || k != 0);
+            };
+            while (left > 0 && ok) {
+                const int lo = cur.step, hi = static_cast<int>(min(static_cast<long long>(cur.steps), lo + left));
+                const bool two = cur.s.n * a.group - cur.mt * G.M > 128;
+                if (!wait(&full[n % NS], (n / NS) & 1u, 3u)) break;
+                for (int h = 0; h < (two ? 2 : 1); ++h) {
+                    if (!wait(&q_ready[h], qp[h], 4u)) break;
+                    qp[h] ^= 1u;
+                    ptx::tc_fence_after();
+                    scores(h, n % NS);
+                    ptx::mma_commit(&s_full[h]);
+                }
+                if (!ok) break;
+                ptx::mma_commit(&empty[n % NS]);
+                for (int st = lo; st < hi; ++st, n += 2) {
+                    const bool more = st + 1 < hi;
+                    const uint32_t vn = n + 1, kn = n + 2;
+                    if (!wait(&full[vn % NS], (vn / NS) & 1u, 3u)) break;
+                    for (int h = 0; h < (two ? 2 : 1); ++h) {
+                        if (!wait(&p_ready[h], pp[h], 5u)) break;
+                        pp[h] ^= 1u;
+                        ptx::tc_fence_after();
+                        values(h, vn % NS, st > lo);
+                        const bool last = h == 1 || !two;
+                        if (last) ptx::mma_commit(&empty[vn % NS]);
+                        if (more) {
+                            if (h == 0 && !wait(&full[kn % NS], (kn / NS) & 1u, 3u)) break;
+                            ptx::tc_fence_after();
+                            scores(h, kn % NS);
+                            ptx::mma_commit(&s_full[h]);
+                            if (last) ptx::mma_commit(&empty[kn % NS]);
+                        } else {
+                            ptx::mma_commit(&o_full[h]);
+                        }
+                    }
+                    if (!ok) break;
+                }
+                left -= hi - lo;
+                if (left > 0) cur.next(a, G);
+            }
+            // every product has finished before TMEM is freed
+            ptx::mma_commit(&drain_bar);
+            const long long t0 = clock64();
+            while (!ptx::mbar_try_wait(&drain_bar, 0) && clock64() - t0 < p.wait_limit) {
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax of one half
+        const int h = warp >> 2, sub = warp & 3;
+        const uint32_t s_t = tmem + h * 128 + (static_cast<uint32_t>(sub * 32) << 16);
+        const uint32_t o_t = s_t - h * 128 + 256 + h * 128;
+        const float scale = fmaxf(fabsf(a.scale_log2), 1.0e-37f);  // (0 would turn what is not seen into NaN)
+        const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;   // a negative scale: q changes sign instead
+        uint32_t sp = 0, op = 0, step_no = 0;
+        bool ok = true;
+        while (left > 0 && ok) {
+            const int lo = cur.step, hi = static_cast<int>(min(static_cast<long long>(cur.steps), lo + left));
+            const SeqInfo s = cur.s;
+            const int rows = s.n * a.group - cur.mt * G.M - h * 128;   // of this half
+            if (rows > 0) {
+                const int r_first = cur.mt * G.M + h * 128;
+                // ---- Q to shared memory: a row per D / 8 lanes, 16 bytes each
+                {
+                    constexpr int LPR = D / 8, RPI = 32 / LPR;
+                    unsigned char* dst = smem + h * S::QHALF;
+                    const int ch = lane % LPR;                     // 16-byte chunk of the row
+#pragma unroll 8
+                    for (int k = 0; k < 32 / RPI; ++k) {
+                        const int r = sub * 32 + k * RPI + lane / LPR;
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (r < rows) {
+                            const int rr = r_first + r, i = rr / a.group;
+                            v = *reinterpret_cast<const uint4*>(a.q + (s.row0 + i) * a.q_stride +
+                                                                static_cast<long long>(cur.h * a.group + rr - i * a.group) * D + ch * 8);
+                            v.x ^= sign; v.y ^= sign; v.z ^= sign; v.w ^= sign;
+                        }
+                        *reinterpret_cast<uint4*>(dst + (ch >> 3) * S::SPAN + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+                    }
+                    ptx::fence_proxy_async_smem();
+                    ptx::mbar_arrive(&q_ready[h]);
+                }
+                const int keys = tile_keys(a, s, cur.mt, G.M);
+                const int rr = r_first + min(sub * 32 + lane, rows - 1);   // this thread's row (or the last one)
+                const int i = rr / a.group;
+                // steps that end in front of this key need no look at what a row sees
+                const int clear = a.mask != nullptr ? s.ctx : s.ctx + r_first / a.group + 1;
+                float m = -INFINITY, l = 0.f;
+                for (int st = lo; st < hi; ++st, ++step_no) {
+                    ok = ptx::mbar_wait(&s_full[h], sp, abort_flag, p.wait_limit, a.status, 6u);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    sp ^= 1u;
+                    ptx::tc_fence_after();
+                    const int c0 = st * TK;
+                    const uint32_t* word = info[step_no % kInfo];
+                    const bool masked = c0 + TK > clear || (word[0] & word[1] & word[2] & word[3]) != 0xFFFFFFFFu;
+                    uint32_t see[4];
+                    if (masked) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) see[q] = seen_bits(a, s, i, c0 + 32 * q, keys) & word[q];
+                    }
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t x[32];
+                        ptx::tmem_ld_32x32b_x32(s_t + q * 32, x);
+                        ptx::tmem_ld_wait(x);
+                        if (masked) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see[q] >> e & 1)) x[e] = 0xFF800000u;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
+                    }
+                    const bool up = (mx - m) * scale > 8.f || (m == -INFINITY && mx > m);
+                    if (__any_sync(0xFFFFFFFFu, up)) {
+                        const float m2 = up ? mx : m;
+                        const float f = up ? tl_ex2((m - m2) * scale) : 1.f;
+                        m = m2;
+                        l *= f;
+                        if (st > lo) {
+                            // O so far (complete: its product came before this step's scores)
+#pragma unroll
+                            for (int q = 0; q < D / 32; ++q) {
+                                uint32_t x[32];
+                                ptx::tmem_ld_32x32b_x32(o_t + q * 32, x);
+                                ptx::tmem_ld_wait(x);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                                ptx::tmem_st_32x32b_x32(o_t + q * 32, x);
+                            }
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m * scale;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t x[32];
+                        ptx::tmem_ld_32x32b_x32(s_t + q * 32, x);
+                        ptx::tmem_ld_wait(x);
+                        if (masked) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see[q] >> e & 1)) x[e] = 0xFF800000u;
+                        }
+                        uint32_t pk[16];
+                        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float u = tl_ex2(fmaf(__uint_as_float(x[e]), scale, -ref));
+                            const float v = tl_ex2(fmaf(__uint_as_float(x[e + 1]), scale, -ref));
+                            l0 += u;
+                            l1 += v;
+                            pk[e / 2] = pack_bf16x2(u, v);
+                        }
+                        l += l0 + l1;
+                        ptx::tmem_st_32x32b_x16(s_t + q * 16, pk);
+                    }
+                    ptx::tmem_st_wait();
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(&p_ready[h]);
+                }
+                if (!ok) break;
+                // ---- epilogue: a thread's row of O
+                ok = ptx::mbar_wait(&o_full[h], op, abort_flag, p.wait_limit, a.status, 8u);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                op ^= 1u;
+                ptx::tc_fence_after();
+                const bool mine = sub * 32 + lane < rows;
+                const int head = cur.h * a.group + rr - i * a.group;
+                const long long row = s.row0 + i;
+                const bool whole = lo == 0 && hi == cur.steps;
+                const size_t slot_row = (2 * static_cast<size_t>(blockIdx.x) + (lo == 0)) * kTileRows + h * 128 + sub * 32 + lane;
+                float* part_o = p.part.o + slot_row * D;
+                float* part_ml = p.part.ml + slot_row * 2;
+                const float inv = l == 0.f ? 0.f : a.c.v_scale / l;
+                bool nan = false;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t x[32];
+                    ptx::tmem_ld_32x32b_x32(o_t + q * 32, x);
+                    ptx::tmem_ld_wait(x);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) nan |= __uint_as_float(x[e]) != __uint_as_float(x[e]);
+                    if (mine && whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + row * a.out_stride + head * D + q * 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                w[j] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(x[e * 8 + 2 * j]) * inv,
+                                                                   __uint_as_float(x[e * 8 + 2 * j + 1]) * inv);
+                            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else if (mine) {
+                        uint4* dst = reinterpret_cast<uint4*>(part_o + q * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dst[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                    }
+                    __syncwarp();
+                }
+                ptx::tc_fence_before();
+                const float m2 = m * scale;
+                if (mine) {
+                    if (!whole) {
+                        part_ml[0] = l == 0.f ? -INFINITY : m2;
+                        part_ml[1] = l;
+                    } else if (a.lse != nullptr) {
+                        a.lse[row * a.n_q + head] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * kLn2F;
+                    }
+                }
+                // 0 * infinity or NaN: a value that the row may not see; again, key by key
+                __syncwarp();
+                uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && nan && l == l && hi * TK > s.ctx);
+                while (again) {
+                    const int src = __ffs(again) - 1;
+                    again &= again - 1;
+                    const int ri = __shfl_sync(0xFFFFFFFFu, i, src), rh = __shfl_sync(0xFFFFFFFFu, head, src);
+                    const size_t sr = slot_row - lane + src;
+                    redo_row<D>(a, cur, ri, rh, lo * TK, min(hi * TK, keys), whole ? nullptr : p.part.o + sr * D,
+                                p.part.ml + sr * 2, lane);
+                }
+            } else {
+                step_no += hi - lo;
+            }
+            left -= hi - lo;
+            if (left > 0) cur.next(a, G);
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch_tiles(const AttnArgs& a, void* partials, int sms, cudaStream_t st) {
+    using S = Tile<D>;
+    TileParams p;
+    p.a = a;
+    const int page = 1 << a.c.page_shift;
+    const int box = page < TK ? page : TK;
+    p.box_shift = page < TK ? a.c.page_shift : 7;
+    p.least = 4;
+    p.wait_limit = 16ll << 30;
+    if (!make_kv_map(&p.tk, a, false, box, false) || !make_kv_map(&p.tv, a, true, box, false)) return cudaErrorInvalidValue;
+    const int blocks = sms < kTileBlocks ? sms : kTileBlocks;
+    p.part.ml = static_cast<float*>(partials);
+    p.part.o = p.part.ml + static_cast<size_t>(2) * kTileBlocks * kTileRows * 2;
+    const cudaError_t e = cudaFuncSetAttribute(tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    {
+        ProfileScope ps("tree_attention", st);
+        tiles_kernel<D><<<blocks, TL_THREADS, S::SMEM, st>>>(p);
+        note_launch();
+    }
+    const cudaError_t le = cudaGetLastError();
+    if (le != cudaSuccess) return le;
+    return launch_tree_attn_join(a, Tiling{kTileRows, TK}, p.part, blocks, p.least, st);
+}
+
+}  // namespace
+
+bool tree_attn_tiles_apply(const AttnArgs& a) {
+    return !a.f8 && a.head_dim <= 128 && static_cast<long long>(a.c.max_new) * a.group > kSmallRows;
+}
+
+cudaError_t launch_tree_attn_tiles(const AttnArgs& a, void* partials, cudaStream_t st) {
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (sms <= 0) sms = 148;
+    return a.head_dim == 64 ? launch_tiles<64>(a, partials, sms, st) : launch_tiles<128>(a, partials, sms, st);
+}
+
+}  // namespace sre
