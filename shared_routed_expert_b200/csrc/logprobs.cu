@@ -39,6 +39,7 @@ constexpr int kCand = 512;               // candidates a block ranks
 constexpr int kMaxC = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+static_assert(kMaxC * kTop <= LP_THREADS && kMaxC * kTop <= kCand, "the join has a thread and a place per alternative");
 
 // order-preserving key: larger values have larger keys, NaN the largest, -0 = +0
 __device__ __forceinline__ uint32_t value_key(float x) {
@@ -103,9 +104,10 @@ struct LpShared {
     unsigned long long top[kTop];        // this block's alternatives, best first
     unsigned long long warp_top[LP_WARPS][32];
     float red[LP_WARPS][4];
+    float4 part[kMaxC];                  // rank 0: the slices' m, l, t, bad
+    float4 sums;                         // this block's maximum, its sums without one maximum, and whether
+                                         // the slice holds NaN or +infinity
     int n_cand;
-    float m, l, t;                       // this block's maximum and sums without one maximum
-    int bad;
 };
 
 // The 32 largest of the block's 512 keys (one per thread), sorted descending, to
@@ -160,7 +162,7 @@ __device__ __forceinline__ unsigned long long block_max(LpShared& sh, unsigned l
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(int V, const char* __restrict__ logits,
+__global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(int V, const char* __restrict__ logits,
                                                               long long row_b, const int32_t* __restrict__ targets,
                                                               int top_n, float* __restrict__ logprobs,
                                                               float* __restrict__ entropy, int32_t* __restrict__ top_ids,
@@ -186,7 +188,6 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(int V, const char*
     const int per_run = max(1, (groups + kG - 1) / kG);
     if (tid == 0) {
         sh.n_cand = 0;
-        sh.bad = 0;
     }
 
     int target = -1;
@@ -201,7 +202,8 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(int V, const char*
     Sums rest{0.f, 0.f}, best{0.f, 0.f};
     int best_g = -1;                     // group of the maximum; -2: the thread's scalar
     float run = -INFINITY;
-    auto account = [&](const float* f, int n, float gm, int g) {
+    auto account = [&](const auto& f, float gm, int g) {
+        constexpr int n = sizeof(f) / sizeof(float);
         // sums of the group against the reference after it
         const float m2 = fmaxf(m, gm);
         const float ref = m2 == -INFINITY ? 0.0f : m2;
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(int V, const char*
             rest.l = l * a;
         }
         float l = 0.f, tt = 0.f;
-#pragma unroll 8
+#pragma unroll
         for (int j = 0; j < n; ++j) {
             const float d = (f[j] - ref) * kLog2e;                 // the difference first: exact near the maximum
             const float e = exp2_fast(d);
@@ -236,8 +238,8 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(int V, const char*
     const int n_tail = V - tail0;
     if (rank == C - 1 && tid >= 32 && tid - 32 < n_tail) scalar = tail0 + tid - 32;
     if (scalar >= 0) {
-        const float f = row.at(scalar);
-        account(&f, 1, f, -2);
+        const float f[1] = {row.at(scalar)};
+        account(f, f[0], -2);
         run = m;
     }
     int run_i = 0;
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(int V, const char*
         float gm = f[0];
 #pragma unroll
         for (int j = 1; j < R::GE; ++j) gm = fmaxf(gm, f[j]);
-        account(f, R::GE, gm, g);
+        account(f, gm, g);
         run = fmaxf(run, gm);
         if ((g + 1) % per_run == 0 || g + 1 == groups) {
             sh.run_max[run_i++][tid] = run;
@@ -338,16 +340,13 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(int V, const char*
             l += sh.red[w][2];
             tt += sh.red[w][3];
         }
-        sh.m = bm;
-        sh.l = l;
-        sh.t = tt;
-        sh.bad = !(l < INFINITY) || bm == INFINITY;                // a NaN or +infinity in the slice
+        sh.sums = make_float4(bm, l, tt, !(l < INFINITY) || bm == INFINITY ? 1.f : 0.f);
     }
     __syncthreads();
 
     // ---- this block's alternatives
     if (top_n > 0) {
-        bool rounds = sh.bad != 0;
+        bool rounds = sh.sums.w != 0.f;
         if (!rounds) {
             // the n-th largest of the threads' maxima (by value alone: key << 32)
             block_top32(sh, static_cast<unsigned long long>(value_key(m)) << 32, warp, lane);
@@ -415,25 +414,32 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(int V, const char*
     if (C > 1) cl.sync();
     else __syncthreads();
     if (rank == 0) {
+        // the slices' sums and alternatives, each read once (the candidates' memory is free)
+        const int all = C * top_n;                                 // at most kMaxC * kTop <= LP_THREADS
+        unsigned long long k = 0;
+        if (tid < all) {
+            k = C > 1 ? cl.map_shared_rank(&sh, tid / top_n)->top[tid % top_n] : sh.top[tid];
+            sh.cand[tid] = k;
+        }
+        if (tid < C) sh.part[tid] = C > 1 ? cl.map_shared_rank(&sh, tid)->sums : sh.sums;
+        __syncthreads();
         float M = -INFINITY;
         bool bad = false;
         for (int r = 0; r < C; ++r) {
-            const LpShared* o = C > 1 ? cl.map_shared_rank(&sh, r) : &sh;
-            M = fmaxf(M, o->m);
-            bad |= o->bad != 0;
+            M = fmaxf(M, sh.part[r].x);
+            bad |= sh.part[r].w != 0.f;
         }
         bad |= M == -INFINITY;
         float L = 0.f, TT = 0.f;
         bool out = false;
         for (int r = 0; r < C; ++r) {
-            const LpShared* o = C > 1 ? cl.map_shared_rank(&sh, r) : &sh;
-            const float om = o->m;
-            if (om == -INFINITY) continue;
-            float ol = o->l, ot = o->t;
-            if (om == M && !out) out = true;                       // the one maximum left out
+            const float4 o = sh.part[r];
+            if (o.x == -INFINITY) continue;
+            float ol = o.y;
+            if (o.x == M && !out) out = true;                      // the one maximum left out
             else ol += 1.0f;
-            const float shift = (om - M) * kLog2e, a = exp2_fast(shift);
-            TT += (ot + ol * shift) * a;
+            const float shift = (o.x - M) * kLog2e, a = exp2_fast(shift);
+            TT += (o.z + ol * shift) * a;
             L += ol * a;
         }
         const float ln1 = log1pf(L);
@@ -443,20 +449,13 @@ __global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(int V, const char*
             if (entropy != nullptr) entropy[t] = bad ? NAN : ln1 - TT * kLn2 / (1.0f + L);
         }
         // rank the slices' alternatives among one another
-        for (int i = tid; i < C * top_n; i += LP_THREADS) {
-            const unsigned long long k = C > 1 ? cl.map_shared_rank(&sh, i / top_n)->top[i % top_n] : sh.top[i];
-            int r = i % top_n;
+        if (k != 0) {
+            int r = tid;
             if (C > 1) {
-                for (int o = 0; o < C; ++o) {
-                    if (o == i / top_n) continue;
-                    const unsigned long long* ot = cl.map_shared_rank(&sh, o)->top;
-                    for (int j = 0; j < top_n; ++j) {
-                        if (ot[j] <= k) break;
-                        ++r;
-                    }
-                }
+                r = 0;
+                for (int j = 0; j < all; ++j) r += sh.cand[j] > k;
             }
-            if (r < top_n && k != 0) {
+            if (r < top_n) {
                 const int id = pair_id(k);
                 top_ids[static_cast<long long>(t) * top_n + r] = id;
                 top_lp[static_cast<long long>(t) * top_n + r] = bad ? NAN : (key_value(static_cast<uint32_t>(k >> 32)) - M) - ln1;

@@ -126,8 +126,9 @@ moe_status moe_qk_norm_rope_append(const moe_kv_cache* cache, const moe_kv_batch
 size_t moe_tree_attention_workspace_size(const moe_kv_cache* cache, int32_t n_q, int32_t T) {
     if (check_cache(cache) != MOE_OK || check_heads(*cache, n_q) != MOE_OK || T < 0 || T > kMaxT) return 0;
     // partial results of the items that a cut between two blocks' shares goes through
-    const size_t rows = kTileBlocks * kTileRows > kSmallBlocks * kSmallRows ? kTileBlocks * kTileRows : kSmallBlocks * kSmallRows;
-    return sizeof(DevStatus) + 2 * rows * (2 + cache->head_dim) * sizeof(float);
+    const size_t small = partials_bytes(kSmallBlocks, kSmallRows, cache->head_dim);
+    const size_t tiles = partials_bytes(kTileBlocks, kTileRows, cache->head_dim);
+    return sizeof(DevStatus) + (small > tiles ? small : tiles);
 }
 
 moe_status moe_tree_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, int32_t T, int32_t n_q,

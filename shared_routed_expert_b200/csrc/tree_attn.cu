@@ -12,43 +12,31 @@ namespace {
 
 constexpr int JN_WARPS = 4;
 
-// Joins the items that a cut between two shares goes through: block x looks at the cut
-// in front of share x + 1 and, if that cut is the first inside its item, joins the
-// item's parts: with M = max m_p, sum_p 2^{m_p - M} (l_p, o_p), in the order of the keys.
-// Bound by latency (a few hundred KB out of L2).
+// Joins the items that a cut between two shares goes through: block x the one that begins
+// in share x and does not end there, with M = max m_p: sum_p 2^{m_p - M} (l_p, o_p), in the
+// order of the keys. A warp per row. Bound by latency (a few hundred KB out of L2), so it is
+// launched early and waits on the device for the kernel before it.
 template <int EPL>
-__global__ void __launch_bounds__(JN_WARPS * 32) join_kernel(const AttnArgs a, const Tiling g, const Partials p, int blocks,
-                                                             int least) {
-    __shared__ ScanShared scan;
-    long long before;
-    int b0, b1;
-    const long long W = scan_steps(a, g, scan, &before, &b0, &b1);
-    const int shares = W > 0 ? share_count(W, blocks, least) : 0;
-    const int cut = blockIdx.x + 1;
-    if (cut >= shares) return;
-    const long long x = share_begin(W, cut, shares);
-    const Cursor c = seek(a, g, scan, x, before, b0, b1);
-    const long long start = x - c.step, end = start + c.steps;
-    if (c.step == 0 || share_begin(W, cut - 1, shares) > start) return;
-    int parts = 1;                                                 // share cut - 1 has the first
-    while (cut + parts - 1 < shares && share_begin(W, cut + parts - 1, shares) < end) ++parts;
+__global__ void __launch_bounds__(JN_WARPS * 32) join_kernel(const AttnArgs a, const int M, const Partials p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const JoinItem c = p.items[blockIdx.x];
+    const int parts = c.parts;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rows = c.s.n * a.group;
-    auto slot = [&](int i) { return i == 0 ? 2 * static_cast<size_t>(cut - 1) + 1 : 2 * static_cast<size_t>(cut - 1 + i); };
-    for (int r = blockIdx.y * JN_WARPS + warp; r < g.M; r += gridDim.y * JN_WARPS) {
-        const int rr = c.mt * g.M + r;
-        if (rr >= rows) break;
+    auto slot = [&](int i) { return 2 * static_cast<size_t>(blockIdx.x + i) + (i == 0); };
+    for (int r = blockIdx.y * JN_WARPS + warp; parts > 0 && r < M; r += gridDim.y * JN_WARPS) {
+        const int rr = c.mt * M + r;
+        if (rr >= c.rows) break;
         float m = -INFINITY;
-        for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.ml[(slot(i) * g.M + r) * 2]);
+        for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.ml[(slot(i) * M + r) * 2]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         const float ref = m == -INFINITY ? 0.f : m;
         float l = 0.f, acc[EPL];
 #pragma unroll
         for (int j = 0; j < EPL; ++j) acc[j] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < parts; ++i) {
-            const size_t at = slot(i) * g.M + r;
+            const size_t at = slot(i) * M + r;
             const float2 v = *reinterpret_cast<const float2*>(p.ml + at * 2);
             const float f = exp2f(v.x - ref);
             const float* o = p.o + at * (32 * EPL) + lane * EPL;
@@ -57,7 +45,7 @@ __global__ void __launch_bounds__(JN_WARPS * 32) join_kernel(const AttnArgs a, c
             for (int j = 0; j < EPL; ++j) acc[j] += o[j] * f;
         }
         const int i = rr / a.group, head = c.h * a.group + rr % a.group;
-        const long long row = c.s.row0 + i;
+        const long long row = c.row0 + i;
         const float inv = l == 0.f ? 0.f : a.c.v_scale / l;
         uint32_t w[EPL / 2];
 #pragma unroll
@@ -111,15 +99,35 @@ bool make_kv_map(CUtensorMap* m, const AttnArgs& a, bool v, int box_rows, bool a
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_tree_attn_join(const AttnArgs& a, Tiling g, Partials p, int blocks, int least, cudaStream_t st) {
+size_t partials_bytes(int blocks, int M, int head_dim) {
+    return (sizeof(JoinItem) * blocks + 255) / 256 * 256 + static_cast<size_t>(2) * blocks * M * (2 + head_dim) * sizeof(float);
+}
+
+Partials partials_at(void* mem, int blocks, int M) {
+    Partials p;
+    p.items = static_cast<JoinItem*>(mem);
+    p.ml = reinterpret_cast<float*>(static_cast<char*>(mem) + (sizeof(JoinItem) * blocks + 255) / 256 * 256);
+    p.o = p.ml + static_cast<size_t>(2) * blocks * M * 2;
+    return p;
+}
+
+cudaError_t launch_tree_attn_join(const AttnArgs& a, int M, Partials p, int blocks, cudaStream_t st) {
     if (blocks < 2) return cudaSuccess;
     ProfileScope ps("tree_attention_join", st);
-    const dim3 grid(blocks - 1, (g.M + 15) / 16);
-    if (a.head_dim == 64) join_kernel<2><<<grid, JN_WARPS * 32, 0, st>>>(a, g, p, blocks, least);
-    else if (a.head_dim == 128) join_kernel<4><<<grid, JN_WARPS * 32, 0, st>>>(a, g, p, blocks, least);
-    else join_kernel<8><<<grid, JN_WARPS * 32, 0, st>>>(a, g, p, blocks, least);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks - 1, (M + JN_WARPS - 1) / JN_WARPS);
+    cfg.blockDim = dim3(JN_WARPS * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = a.head_dim == 64    ? cudaLaunchKernelEx(&cfg, join_kernel<2>, a, M, p)
+                          : a.head_dim == 128 ? cudaLaunchKernelEx(&cfg, join_kernel<4>, a, M, p)
+                                              : cudaLaunchKernelEx(&cfg, join_kernel<8>, a, M, p);
     note_launch();
-    return cudaGetLastError();
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace sre

@@ -249,12 +249,25 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnArgs& a, const SeqInfo& 
     return bits;
 }
 
+// What is left to join of an item that begins in a block's share and ends in a later one.
+struct JoinItem {
+    int parts;                           // shares that hold a part of it; 0: nothing to join
+    int row0, rows;                      // of the sequence: first row, packed rows of a kv head
+    int h, mt;
+};
+
 // Partial results of a share: slot 2 * block + 1 for an item that begins in the block's
 // share, 2 * block for one that began before it.
 struct Partials {
+    JoinItem* items;                     // [blocks]
     float* ml;                           // [slots][M][2]: maximum (base 2), sum
     float* o;                            // [slots][M][head_dim]
 };
+
+// shares from the one numbered `share` up to the one that holds the last of steps [.., end)
+__device__ __forceinline__ int parts_until(long long W, int shares, int share, long long end) {
+    return static_cast<int>((shares * end + W - 1) / W) - share;
+}
 
 constexpr int kSmallBlocks = 320;        // most blocks of the 16- to 64-row kernel
 constexpr int kSmallRows = 64;
@@ -262,7 +275,10 @@ constexpr int kTileBlocks = 160;         // most blocks of the 256-row kernel
 constexpr int kTileRows = 256;
 
 cudaError_t launch_tree_attn_small(const AttnArgs& a, void* partials, cudaStream_t st);
-cudaError_t launch_tree_attn_join(const AttnArgs& a, Tiling g, Partials p, int blocks, int least, cudaStream_t st);
+cudaError_t launch_tree_attn_join(const AttnArgs& a, int M, Partials p, int blocks, cudaStream_t st);
+// where the partial results of up to `blocks` blocks with tiles of M rows lie in memory
+Partials partials_at(void* mem, int blocks, int M);
+size_t partials_bytes(int blocks, int M, int head_dim);
 bool make_kv_map(CUtensorMap* m, const AttnArgs& a, bool v, int box_rows, bool all_spans);
 bool tree_attn_tiles_apply(const AttnArgs& a);
 cudaError_t launch_tree_attn_tiles(const AttnArgs& a, void* partials, cudaStream_t st);

@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
     int b0, b1;
     const long long W = scan_steps(a, G, scan, &before, &b0, &b1);         // (synchronises)
     const int shares = W > 0 ? share_count(W, gridDim.x, p.least) : 0;
+    if (threadIdx.x == 0) p.part.items[blockIdx.x].parts = 0;
     if (static_cast<int>(blockIdx.x) >= shares) return;
     const long long x0 = share_begin(W, blockIdx.x, shares), x1 = share_begin(W, blockIdx.x + 1, shares);
     Cursor cur = seek(a, G, scan, x0, before, b0, b1);
@@ -484,6 +485,8 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
         compute_sync();
         const bool whole = lo == 0 && hi == cur.steps;
         const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (lo == 0);
+        if (threadIdx.x == 0 && lo == 0 && !whole)                 // (the last of the share, so left == hi)
+            p.part.items[blockIdx.x] = JoinItem{parts_until(W, shares, blockIdx.x, x1 - hi + cur.steps), s.row0, rows, cur.h, cur.mt};
         for (int r = warp; r < M; r += 4) {
             const int rr = cur.mt * M + r;
             if (rr >= rows) break;
@@ -558,8 +561,7 @@ cudaError_t launch_cfg(const AttnArgs& a, void* partials, int sms, cudaStream_t 
     p.wait_limit = 4ll << 30;
     if (!make_kv_map(&p.tk, a, false, box, true) || !make_kv_map(&p.tv, a, true, box, true)) return cudaErrorInvalidValue;
     const int blocks = sms * S::BLOCKS_PER_SM < kSmallBlocks ? sms * S::BLOCKS_PER_SM : kSmallBlocks;
-    p.part.ml = static_cast<float*>(partials);
-    p.part.o = p.part.ml + static_cast<size_t>(2) * kSmallBlocks * kSmallRows * 2;
+    p.part = partials_at(partials, blocks, S::M);
     const cudaError_t e = cudaFuncSetAttribute(small_kernel<D, F8, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
     {
@@ -569,7 +571,7 @@ cudaError_t launch_cfg(const AttnArgs& a, void* partials, int sms, cudaStream_t 
     }
     const cudaError_t le = cudaGetLastError();
     if (le != cudaSuccess) return le;
-    return launch_tree_attn_join(a, Tiling{S::M, S::SK}, p.part, blocks, p.least, st);
+    return launch_tree_attn_join(a, S::M, p.part, blocks, st);
 }
 
 template <int D, bool F8>

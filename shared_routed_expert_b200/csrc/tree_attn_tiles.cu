@@ -117,6 +117,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
     int b0, b1;
     const long long W = scan_steps(a, G, scan, &before, &b0, &b1);
     const int shares = W > 0 ? share_count(W, gridDim.x, p.least) : 0;
+    if (threadIdx.x == 0) p.part.items[blockIdx.x].parts = 0;
     if (static_cast<int>(blockIdx.x) >= shares) return;
     const long long x0 = share_begin(W, blockIdx.x, shares), x1 = share_begin(W, blockIdx.x + 1, shares);
     Cursor cur = seek(a, G, scan, x0, before, b0, b1);
@@ -426,6 +427,9 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                 const long long row = s.row0 + i;
                 const bool whole = lo == 0 && hi == cur.steps;
                 const size_t slot_row = (2 * static_cast<size_t>(blockIdx.x) + (lo == 0)) * kTileRows + h * 128 + sub * 32 + lane;
+                if (threadIdx.x == 0 && lo == 0 && !whole)         // (the last of the share; half 0 always has rows)
+                    p.part.items[blockIdx.x] =
+                        JoinItem{parts_until(W, shares, blockIdx.x, x1 - hi + cur.steps), s.row0, s.n * a.group, cur.h, cur.mt};
                 float* part_o = p.part.o + slot_row * D;
                 float* part_ml = p.part.ml + slot_row * 2;
                 const float inv = l == 0.f ? 0.f : a.c.v_scale / l;
@@ -504,8 +508,7 @@ cudaError_t launch_tiles(const AttnArgs& a, void* partials, int sms, cudaStream_
     p.wait_limit = 16ll << 30;
     if (!make_kv_map(&p.tk, a, false, box, false) || !make_kv_map(&p.tv, a, true, box, false)) return cudaErrorInvalidValue;
     const int blocks = sms < kTileBlocks ? sms : kTileBlocks;
-    p.part.ml = static_cast<float*>(partials);
-    p.part.o = p.part.ml + static_cast<size_t>(2) * kTileBlocks * kTileRows * 2;
+    p.part = partials_at(partials, blocks, kTileRows);
     const cudaError_t e = cudaFuncSetAttribute(tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
     {
@@ -515,7 +518,7 @@ cudaError_t launch_tiles(const AttnArgs& a, void* partials, int sms, cudaStream_
     }
     const cudaError_t le = cudaGetLastError();
     if (le != cudaSuccess) return le;
-    return launch_tree_attn_join(a, Tiling{kTileRows, TK}, p.part, blocks, p.least, st);
+    return launch_tree_attn_join(a, kTileRows, p.part, blocks, st);
 }
 
 }  // namespace
