@@ -156,6 +156,13 @@ moe_status moe_tree_attention(const moe_kv_cache* cache, const moe_kv_batch* bat
     a.T = T;
     a.n_q = n_q;
     a.group = n_q / cache->n_kv;
+    {   // ceil(2^(31 + s) / group) with 2^s >= group: exact for numerators below 2^31
+        int s = 0;
+        while ((1 << s) < a.group) ++s;
+        const uint64_t mul = ((uint64_t{1} << (31 + s)) + a.group - 1) / a.group;
+        a.group_mul = static_cast<uint32_t>(a.group == 1 ? 0 : mul);
+        a.group_shift = s > 0 ? s - 1 : 0;
+    }
     a.head_dim = cache->head_dim;
     a.f8 = cache->dtype == MOE_E4M3;
     a.scale_log2 = softmax_scale * cache->k_scale * kLog2E;

@@ -10,6 +10,7 @@ namespace sre {
 struct AttnArgs {
     KvView c;
     int T, n_q, group;                   // group: query heads per kv head
+    uint32_t group_mul, group_shift;     // r / group = mulhi(r, group_mul) >> group_shift for 0 <= r < 2^31
     int head_dim;
     bool f8;
     float scale_log2;                    // softmax_scale * k_scale * log2(e)
@@ -22,6 +23,10 @@ struct AttnArgs {
     float* lse;
     DevStatus* status;
 };
+
+__device__ __forceinline__ int token_of(const AttnArgs& a, int r) {
+    return a.group == 1 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), a.group_mul) >> a.group_shift);
+}
 
 // new rows that a sequence may have (rows behind the mask's columns are refused)
 __device__ __forceinline__ int attn_max_new(const AttnArgs& a) {
@@ -84,21 +89,21 @@ __device__ __forceinline__ void attend_row(const AttnArgs& a, int b, const SeqIn
 // ---- splitting the work
 // An item is (sequence, kv head, tile of M query rows); the rows of a kv head are
 // packed token-major, row r being token r / group, query head r % group. An item takes
-// steps of SK keys up to the last key that one of its rows may see. The steps of all
-// items, in the order sequence, head, tile, are one axis that is cut into equal shares,
-// one per block, so the load is even whatever the lengths; an item that a cut goes
-// through leaves partial results (unnormalised sums with their maximum) that are joined
-// afterwards in the order of the keys.
+// steps of SK keys up to the last key that one of its rows may see, and as much time as
+// `extra` steps more for its beginning and end. These units of all items, in the order
+// sequence, head, tile, are one axis that is cut into equal shares, one per block, so the
+// load is even whatever the lengths; an item that a cut goes through leaves partial results
+// (unnormalised sums with their maximum) that are joined in the order of the keys.
 
 struct Tiling {
-    int M, SK;
+    int M, SK, extra;
 };
 
 // last cache index + 1 that rows of tile mt may see
 __device__ __forceinline__ int tile_keys(const AttnArgs& a, const SeqInfo& s, int mt, int M) {
     if (a.mask != nullptr) return s.ctx + s.n;
     const int last = min((mt + 1) * M, s.n * a.group) - 1;
-    return s.ctx + last / a.group + 1;
+    return s.ctx + token_of(a, last) + 1;
 }
 __device__ __forceinline__ int tile_steps(const AttnArgs& a, const SeqInfo& s, int mt, Tiling g) {
     return (tile_keys(a, s, mt, g.M) + g.SK - 1) / g.SK;
@@ -106,16 +111,38 @@ __device__ __forceinline__ int tile_steps(const AttnArgs& a, const SeqInfo& s, i
 __device__ __forceinline__ int seq_tiles(const AttnArgs& a, const SeqInfo& s, int M) {
     return (s.n * a.group + M - 1) / M;
 }
-// steps of one kv head of a sequence
-__device__ __forceinline__ long long head_steps(const AttnArgs& a, const SeqInfo& s, Tiling g) {
+// units of one kv head of a sequence
+__device__ __forceinline__ long long head_units(const AttnArgs& a, const SeqInfo& s, Tiling g) {
     const int tiles = seq_tiles(a, s, g.M);
     if (tiles == 0) return 0;
     const int lo = tile_steps(a, s, 0, g), hi = tile_steps(a, s, tiles - 1, g);
-    if (lo == hi) return static_cast<long long>(tiles) * lo;
+    if (lo == hi) return static_cast<long long>(tiles) * (lo + g.extra);
     long long sum = 0;
-    for (int mt = 0; mt < tiles; ++mt) sum += tile_steps(a, s, mt, g);
+    for (int mt = 0; mt < tiles; ++mt) sum += tile_steps(a, s, mt, g) + g.extra;
     return sum;
 }
+
+__device__ __forceinline__ long long div_pos(long long a, long long b) {       // a >= 0, b > 0
+    return ((a | b) >> 31) ? a / b : static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
+// W units cut into `count` shares, the first `longer` of them a unit longer.
+struct Shares {
+    int count, longer;
+    long long base;
+
+    __device__ __forceinline__ Shares(long long W, int blocks, int least) {
+        const long long most = div_pos(W + least - 1, least);
+        count = static_cast<int>(most < blocks ? most : blocks);
+        base = count > 0 ? div_pos(W, count) : 0;
+        longer = static_cast<int>(W - base * count);
+    }
+    __device__ __forceinline__ long long begin(int i) const { return i * base + min(i, longer); }
+    __device__ __forceinline__ int of(long long x) const {                     // the share that holds unit x
+        const long long head = longer * (base + 1);
+        return static_cast<int>(x < head ? div_pos(x, base + 1) : longer + div_pos(x - head, base));
+    }
+};
 
 struct ScanShared {
     long long warp_sum[32];
@@ -123,17 +150,9 @@ struct ScanShared {
     int b;
 };
 
-// Number of blocks that share W steps: no more than `blocks`, and no share below
-// `least` steps.
-__device__ __forceinline__ int share_count(long long W, int blocks, int least) {
-    const long long n = (W + least - 1) / least;
-    return static_cast<int>(n < blocks ? (n > 1 ? n : 1) : blocks);
-}
-__device__ __forceinline__ long long share_begin(long long W, int i, int count) { return W * i / count; }
-
-// All steps of the call (W); called by every thread of the block. *before: steps in
-// front of this thread's sequences.
-__device__ __forceinline__ long long scan_steps(const AttnArgs& a, Tiling g, ScanShared& sh, long long* before, int* b0,
+// All units of the call; called by every thread of the block. *before: units in front of
+// this thread's sequences [*b0, *b1).
+__device__ __forceinline__ long long scan_units(const AttnArgs& a, Tiling g, ScanShared& sh, long long* before, int* b0,
                                                 int* b1) {
     const int per = (a.c.B + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
     *b0 = min(a.c.B, static_cast<int>(threadIdx.x) * per);
@@ -141,8 +160,8 @@ __device__ __forceinline__ long long scan_steps(const AttnArgs& a, Tiling g, Sca
     long long mine = 0;
     for (int b = *b0; b < *b1; ++b) {
         const SeqInfo s = seq_info(a.c, b, a.T, attn_max_new(a));
-        if (!s.ok && blockIdx.x == 0 && blockIdx.y == 0) report(a.status, MOE_ERR_DEVICE, b);
-        mine += head_steps(a, s, g) * a.c.n_kv;
+        if (!s.ok && blockIdx.x == 0) report(a.status, MOE_ERR_DEVICE, b);
+        mine += head_units(a, s, g) * a.c.n_kv;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     long long inc = mine;
@@ -162,15 +181,14 @@ __device__ __forceinline__ long long scan_steps(const AttnArgs& a, Tiling g, Sca
     return W;
 }
 
-// A place on the axis: an item and the step within it.
+// A place on the axis: an item and the unit within it.
 struct Cursor {
     SeqInfo s;
-    int b, h, mt, step, steps;           // steps: of the whole item
+    int b, h, mt, unit, steps;           // steps: of the whole item
 
-    __device__ __forceinline__ void open(const AttnArgs& a, Tiling g) { steps = tile_steps(a, s, mt, g); }
-    // to the first step of the next item (sequences without steps are passed over)
+    // to the first unit of the next item (sequences without rows are passed over)
     __device__ __forceinline__ void next(const AttnArgs& a, Tiling g) {
-        step = 0;
+        unit = 0;
         if (++mt >= seq_tiles(a, s, g.M)) {
             mt = 0;
             if (++h >= a.c.n_kv) {
@@ -182,17 +200,31 @@ struct Cursor {
                 } while (s.n == 0);
             }
         }
-        open(a, g);
+        steps = tile_steps(a, s, mt, g);
+    }
+    // Moves on to the next item with steps inside the share (`left` units from here): its
+    // steps [lo, hi); false at the end of the share. The cursor then stands behind hi.
+    __device__ __forceinline__ bool segment(const AttnArgs& a, Tiling g, long long& left, int& lo, int& hi) {
+        while (left > 0) {
+            if (unit >= g.extra + steps) next(a, g);
+            const int to = static_cast<int>(min(static_cast<long long>(g.extra + steps), unit + left));
+            lo = max(0, unit - g.extra);
+            hi = max(0, to - g.extra);
+            left -= to - unit;
+            unit = to;
+            if (hi > lo) return true;
+        }
+        return false;
     }
 };
 
-// The place of step x (0 <= x < W), by every thread of the block, after scan_steps.
+// The place of unit x (0 <= x < W), by every thread of the block, after scan_units.
 __device__ __forceinline__ Cursor seek(const AttnArgs& a, Tiling g, ScanShared& sh, long long x, long long before, int b0,
                                        int b1) {
     if (x >= before) {
         long long rem = x - before;
         for (int b = b0; b < b1; ++b) {
-            const long long n = head_steps(a, seq_info(a.c, b, a.T, attn_max_new(a)), g) * a.c.n_kv;
+            const long long n = head_units(a, seq_info(a.c, b, a.T, attn_max_new(a)), g) * a.c.n_kv;
             if (rem < n) {
                 sh.b = b;
                 sh.rem = rem;
@@ -205,23 +237,32 @@ __device__ __forceinline__ Cursor seek(const AttnArgs& a, Tiling g, ScanShared& 
     Cursor c;
     c.b = sh.b;
     c.s = seq_info(a.c, c.b, a.T, attn_max_new(a));
-    const long long per = head_steps(a, c.s, g);
-    c.h = static_cast<int>(sh.rem / per);
-    long long rem = sh.rem % per;
+    const long long per = head_units(a, c.s, g);
+    c.h = static_cast<int>(div_pos(sh.rem, per));
+    long long rem = sh.rem - c.h * per;
     c.mt = 0;
-    c.open(a, g);
-    if (per == static_cast<long long>(c.steps) * seq_tiles(a, c.s, g.M)) {
-        c.mt = static_cast<int>(rem / c.steps);
-        rem %= c.steps;
+    c.steps = tile_steps(a, c.s, 0, g);
+    const int units = c.steps + g.extra;
+    if (per == static_cast<long long>(units) * seq_tiles(a, c.s, g.M)) {
+        c.mt = static_cast<int>(div_pos(rem, units));
+        rem -= static_cast<long long>(c.mt) * units;
     } else {
-        while (rem >= c.steps) {
-            rem -= c.steps;
+        while (rem >= c.steps + g.extra) {
+            rem -= c.steps + g.extra;
             ++c.mt;
-            c.open(a, g);
+            c.steps = tile_steps(a, c.s, c.mt, g);
         }
     }
-    c.step = static_cast<int>(rem);
+    c.unit = static_cast<int>(rem);
     return c;
+}
+
+// The shares that hold steps of the item that a cursor behind some of its units stands in
+// (`end`: the share's end, `left`: what is left of it): the first one and their number.
+__device__ __forceinline__ int2 item_shares(const Shares& sh, const Cursor& c, Tiling g, long long end, long long left) {
+    const long long start = end - left - c.unit + g.extra;
+    const int first = sh.of(start);
+    return make_int2(first, sh.of(start + c.steps - 1) - first + 1);
 }
 
 // Keys c0 .. c0 + 31 that row (token i) of a sequence sees, as bits, of those below `end`
@@ -259,14 +300,55 @@ struct JoinItem {
 // Partial results of a share: slot 2 * block + 1 for an item that begins in the block's
 // share, 2 * block for one that began before it.
 struct Partials {
+    unsigned* arrived;                   // [blocks] parts of the item that begins in a share; 0 between calls
     JoinItem* items;                     // [blocks]
     float* ml;                           // [slots][M][2]: maximum (base 2), sum
     float* o;                            // [slots][M][head_dim]
 };
 
-// shares from the one numbered `share` up to the one that holds the last of steps [.., end)
-__device__ __forceinline__ int parts_until(long long W, int shares, int share, long long end) {
-    return static_cast<int>((shares * end + W - 1) / W) - share;
+// Row r of a tile of M rows (rr of the item's packed rows) from its parts in `parts` shares
+// from `first` on, by one warp: with m = max m_p, sum_p 2^{m_p - m} (l_p, o_p).
+template <int EPL>
+__device__ __forceinline__ void join_row(const AttnArgs& a, const Partials& p, int M, int first, int parts, int row0, int h,
+                                         int r, int rr, int lane) {
+    auto slot = [&](int i) { return 2 * static_cast<size_t>(first + i) + (i == 0); };
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(p.ml + (slot(i) * M + r) * 2));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f, acc[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) acc[j] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const size_t at = slot(i) * M + r;
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ml + at * 2));
+        const float f = exp2f(v.x - ref);
+        float o[EPL];
+        if constexpr (EPL == 2) {
+            *reinterpret_cast<float2*>(o) = __ldcg(reinterpret_cast<const float2*>(p.o + at * 64) + lane);
+        } else {
+#pragma unroll
+            for (int q = 0; q < EPL / 4; ++q)
+                *reinterpret_cast<float4*>(o + 4 * q) =
+                    __ldcg(reinterpret_cast<const float4*>(p.o + at * (32 * EPL)) + lane * (EPL / 4) + q);
+        }
+        l += v.y * f;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) acc[j] += o[j] * f;
+    }
+    const int i = token_of(a, rr), head = h * a.group + rr - i * a.group;
+    const long long row = row0 + i;
+    const float inv = l == 0.f ? 0.f : a.c.v_scale / l;
+    uint32_t w[EPL / 2];
+#pragma unroll
+    for (int j = 0; j < EPL; j += 2) w[j / 2] = l == 0.f ? 0u : pack_bf16x2(acc[j] * inv, acc[j + 1] * inv);
+    uint16_t* dst = a.out + row * a.out_stride + head * (32 * EPL) + lane * EPL;
+    if constexpr (EPL == 2) *reinterpret_cast<uint32_t*>(dst) = w[0];
+    else if constexpr (EPL == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[EPL / 2 - 2], w[EPL / 2 - 1]);
+    if (a.lse != nullptr && lane == 0) a.lse[row * a.n_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2F;
 }
 
 constexpr int kSmallBlocks = 320;        // most blocks of the 16- to 64-row kernel
@@ -279,7 +361,7 @@ cudaError_t launch_tree_attn_join(const AttnArgs& a, int M, Partials p, int bloc
 // where the partial results of up to `blocks` blocks with tiles of M rows lie in memory
 Partials partials_at(void* mem, int blocks, int M);
 size_t partials_bytes(int blocks, int M, int head_dim);
-bool make_kv_map(CUtensorMap* m, const AttnArgs& a, bool v, int box_rows, bool all_spans);
+bool make_kv_map(CUtensorMap* m, const AttnArgs& a, bool v, int box_rows);
 bool tree_attn_tiles_apply(const AttnArgs& a);
 cudaError_t launch_tree_attn_tiles(const AttnArgs& a, void* partials, cudaStream_t st);
 

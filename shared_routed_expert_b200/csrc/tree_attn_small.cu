@@ -2,12 +2,17 @@
 // bound by reading the cache once.
 //
 // Flash decoding with warp-level matrix instructions: a block takes tiles of M = 16, 32
-// or 64 packed query rows and runs along its share of the key axis (tree_attn.cuh). A
-// producer warp streams chunks of 32 keys (K and V rows, one TMA box per page piece)
-// through a ring in shared memory; 4 / WM groups of WM warps take the chunks in turn,
-// each warp 16 rows, with its own running maximum and sum, so warps meet only at the end
-// of an item. Scores and the output accumulate in fp32 registers (m16n8k16); P is rounded
-// to 16 bits as the second product's operand.
+// or 64 packed query rows and runs along its share of the key axis (tree_attn.cuh). Its 8
+// warps form 8 / WM groups of WM warps; the groups take chunks of CK keys in turn, each
+// warp 16 rows, with its own running maximum and sum, so groups meet only at the end of an
+// item. Each group has a ring of its own in shared memory that its first warp fills by TMA
+// (one box per page piece and 128-byte span), K and V apart: the next K is on its way as
+// soon as the scores are formed. Scores and the output accumulate in fp32 registers
+// (m16n8k16); P is rounded to 16 bits as the second product's operand. What a warp does for
+// a chunk is one chain of dependent steps, so warps are what hides latency: two blocks of 8
+// per SM, with Q in shared memory to leave a thread within 128 registers, and no warp spent
+// on loads alone (two blocks of 4 warps and a loading warp, Q in registers: 158 us for 64
+// decode rows of 96 heads over 544 MB of E4M3 cache, 223 us for 128 rows over 566 MB bf16).
 //   bf16 cache: Q, K, P, V as bf16.
 //   E4M3 cache: K and V codes convert to fp16 exactly; Q rows are scaled by a power of two
 //   to fp16 (exact for everything within 2^-28 of the row's largest entry) and P is fp16.
@@ -24,20 +29,27 @@ namespace sre {
 
 namespace {
 
-constexpr int CK = 32;                   // keys per chunk
-constexpr int SM_THREADS = 160;          // 4 compute warps and the producer
+constexpr int NW = 8;                    // compute warps
+constexpr int SM_THREADS = 32 * NW;
 
 template <int D, bool F8, int WM>
 struct Small {
     static constexpr int ESZ = F8 ? 1 : 2;
-    static constexpr int M = 16 * WM, WK = 4 / WM, SK = CK * WK;
+    // keys per chunk: 32 where a group's ring holds K and V of that many
+    static constexpr int CK = WM == 1 && D * ESZ >= (D == 256 ? 512 : 256) ? 16 : 32;
+    static constexpr int M = 16 * WM, WK = NW / WM, SK = CK * WK;
     static constexpr int ROWB = D * ESZ < 128 ? D * ESZ : 128;     // bytes of a row within one swizzle span
-    static constexpr int KBYTES = CK * D * ESZ;                    // K (or V) of a chunk
-    static constexpr int STAGE = 2 * KBYTES;
-    static constexpr int RING = D == 256 ? 131072 : (D * ESZ == 64 ? 49152 : 65536);
-    static constexpr int NS = RING / STAGE;
+    static constexpr int SPANS = D * ESZ / ROWB;
+    static constexpr int SPAN = CK * ROWB;                         // a chunk is stored [span][key][ROWB], swizzled
+    static constexpr int KBYTES = SPANS * SPAN;                    // K (or V) of a chunk
+    static constexpr int RING = D == 256 ? 131072 : 65536;
+    static constexpr int NG = RING / (WK * 2 * KBYTES) < 4 ? RING / (WK * 2 * KBYTES) : 4;   // chunks a group holds
+    static_assert(NG >= 1, "a group's ring holds a chunk");
+    static constexpr int EXTRA = WM == 4 ? 2 : 1;                  // what an item costs besides its steps, in steps
     static constexpr int PITCH = D + 8;                            // floats per row of the merge buffer
-    static constexpr int BUF = WK * M * PITCH * 4;
+    static constexpr int BUF = WK / 2 * M * PITCH * 4;             // half of the groups' results
+    static constexpr int QPITCH = D * 2 + 16;                      // bytes per row of Q, which lies there before
+    static_assert(M * QPITCH <= BUF, "Q fits the merge buffer");
     static constexpr int SMEM = RING + BUF + 1024;
     static constexpr int BLOCKS_PER_SM = D == 256 ? 1 : 2;
 };
@@ -47,7 +59,6 @@ struct SmallParams {
     CUtensorMap tk, tv;
     Partials part;
     int box_shift;                       // log2 of the rows of a TMA box
-    int least;                           // smallest share, in steps
     long long wait_limit;
 };
 
@@ -85,206 +96,216 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// What a group loads of an item: its chunks start at key `first` and lie SK keys apart.
+struct Chunks {
+    const int32_t* table;
+    int b, h, first, keys, n;
+};
 
 template <int D, bool F8, int WM>
 __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM)) small_kernel(
     const __grid_constant__ SmallParams p) {
     using S = Small<D, F8, WM>;
-    constexpr int NS = S::NS, WK = S::WK, M = S::M, EPL = D / 32;
-    constexpr Tiling G{M, S::SK};
+    constexpr int WK = S::WK, M = S::M, EPL = D / 32, CK = S::CK, NG = S::NG;
+    constexpr Tiling G{M, S::SK, S::EXTRA};
+    constexpr uint32_t ALL = CK == 32 ? 0xFFFFFFFFu : 0xFFFFu;     // a chunk's keys as bits
     extern __shared__ __align__(1024) unsigned char sm_raw[];
     __shared__ ScanShared scan;
-    __shared__ uint64_t full[NS], empty[NS];
-    __shared__ uint32_t valid[NS];       // keys of the chunk that were loaded
-    __shared__ float ml[WK * M][2];
-    __shared__ int s_abort, s_stop;
+    __shared__ uint64_t kfull[WK][NG], vfull[WK][NG], kfree[WK][NG], vfree[WK][NG];
+    __shared__ uint32_t valid[WK][NG];   // keys of the chunk that were loaded
+    __shared__ float ml[NW * 16][2];
+    __shared__ float q_scale[M];         // E4M3: what a row of Q was divided by, times the scale
+    __shared__ int s_abort, s_stop, s_last;
     unsigned char* ring = sm_raw + ((1024 - (ptx::smem_u32(sm_raw) & 1023)) & 1023);
     float* buf = reinterpret_cast<float*>(ring + S::RING);
+    unsigned char* q_smem = ring + S::RING;                        // (before the merge)
     volatile int* abort_flag = &s_abort;
     const AttnArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         s_abort = 0;
-        for (int i = 0; i < NS; ++i) {
-            ptx::mbar_init(&full[i], 1);
-            ptx::mbar_init(&empty[i], WM);
-        }
+        for (int i = 0; i < WK; ++i)
+            for (int j = 0; j < NG; ++j) {
+                ptx::mbar_init(&kfull[i][j], 1);
+                ptx::mbar_init(&vfull[i][j], 1);
+                ptx::mbar_init(&kfree[i][j], WM);
+                ptx::mbar_init(&vfree[i][j], WM);
+            }
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&p.tk);
         ptx::prefetch_tmap(&p.tv);
     }
     long long before;
     int b0, b1;
-    const long long W = scan_steps(a, G, scan, &before, &b0, &b1);         // (synchronises)
-    const int shares = W > 0 ? share_count(W, gridDim.x, p.least) : 0;
-    if (threadIdx.x == 0) p.part.items[blockIdx.x].parts = 0;
-    if (static_cast<int>(blockIdx.x) >= shares) return;
-    const long long x0 = share_begin(W, blockIdx.x, shares), x1 = share_begin(W, blockIdx.x + 1, shares);
+    const long long W = scan_units(a, G, scan, &before, &b0, &b1);         // (synchronises)
+    const Shares shares(W, gridDim.x, 1 + S::EXTRA);
+    if (static_cast<int>(blockIdx.x) >= shares.count) return;
+    const long long x0 = shares.begin(blockIdx.x), x1 = shares.begin(blockIdx.x + 1);
     Cursor cur = seek(a, G, scan, x0, before, b0, b1);
     long long left = x1 - x0;
+    int lo, hi;
+    if (!cur.segment(a, G, left, lo, hi)) return;
 
-    if (warp == 4) {
-        // ------------------------------------------------------------ producer
-        const int box = 1 << p.box_shift, pieces = CK >> p.box_shift;
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        while (left > 0 && ok) {
-            const int lo = cur.step, hi = static_cast<int>(min(static_cast<long long>(cur.steps), lo + left));
-            const int keys = tile_keys(a, cur.s, cur.mt, M);
-            const int32_t* table = a.c.page_table + static_cast<size_t>(cur.b) * a.c.max_pages;
-            // lane l holds the page of piece base + l; the next 32 are fetched ahead
-            const int first = lo * S::SK, stop = min(hi * S::SK, keys);
-            auto fetch = [&](int piece) {
-                const int c = first + ((piece + lane) << p.box_shift);
-                return c < stop ? table[c >> a.c.page_shift] : -1;
-            };
-            int base = 0;
-            int page_now = fetch(0), page_next = fetch(32);
-            for (int chunk = lo * WK; chunk < hi * WK && ok; ++chunk) {
-                const int c0 = chunk * CK;
-                const int at = (c0 - first) >> p.box_shift;
-                if (at - base >= 32) {
-                    base += 32;
-                    page_now = page_next;
-                    page_next = fetch(base + 32);
-                }
-                const int pg0 = __shfl_sync(0xFFFFFFFFu, page_now, (at - base) & 31);
-                const int pg1 = __shfl_sync(0xFFFFFFFFu, page_now, (at - base + 1) & 31);
-                if (lane == 0) {
-                    ok = ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.wait_limit, a.status, 1u);
-                    if (ok) {
-                        uint32_t v = 0;
-                        bool good[2] = {false, false};
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const int c = c0 + q * box;
-                            if (q >= pieces || c >= keys) continue;
-                            const int pg = q ? pg1 : pg0;
-                            good[q] = pg >= 0 && pg < a.c.num_pages;
-                            if (!good[q]) report(a.status, MOE_ERR_DEVICE, cur.b);
-                            else v |= (box == 32 ? 0xFFFFFFFFu : 0xFFFFu) << (q * 16);
-                        }
-                        const int rest = keys - c0;
-                        if (rest < 32) v &= rest <= 0 ? 0u : (1u << rest) - 1u;
-                        valid[stage] = v;
-                        const uint32_t bytes = (static_cast<uint32_t>(good[0]) + good[1]) * 2u * box * D * S::ESZ;
-                        ptx::mbar_arrive_expect_tx(&full[stage], bytes);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            if (!good[q]) continue;
-                            unsigned char* dst = ring + stage * S::STAGE + q * box * D * S::ESZ;
-                            const int slot = (c0 + q * box) & ((1 << a.c.page_shift) - 1), pg = q ? pg1 : pg0;
-                            ptx::tma_load_5d(dst, &p.tk, &full[stage], 0, slot, 0, cur.h, pg);
-                            ptx::tma_load_5d(dst + S::KBYTES, &p.tv, &full[stage], 0, slot, 0, cur.h, pg);
-                        }
-                    }
-                }
-                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-                if (++stage == NS) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-            left -= hi - lo;
-            if (left > 0) cur.next(a, G);
-        }
-        if (lane == 0 && *abort_flag) {
-            // every copy in flight lands before the block's memory goes away: stages below
-            // `stage` were armed in this round, the others in the one before, if ever
-            for (int i = 0; i < NS; ++i) {
-                const uint32_t par = i < stage ? phase : phase ^ 1u;
-                const long long t0 = clock64();
-                while (!ptx::mbar_try_wait(&full[i], par) && clock64() - t0 < p.wait_limit) {
-                }
-            }
-        }
-        return;
-    }
-
-    // ---------------------------------------------------------------- compute warps
     const int wm = warp % WM, wk = warp / WM;
+    const bool leads = wm == 0;
     const int g = lane >> 2, t = lane & 3;
-    const int box = 1 << p.box_shift;
-    const uint32_t ring_u = ptx::smem_u32(ring);
+    unsigned char* mem = ring + wk * NG * 2 * S::KBYTES;           // this group's ring: K, V, K, V, ...
+    const uint32_t mem_u = ptx::smem_u32(mem);
     const bool flip = a.scale_log2 < 0.f;                          // a negative scale: q changes sign instead
     const float scale = fabsf(a.scale_log2);
-    // swizzled addresses: row r of a piece begins at r * ROWB, its 16-byte chunk c lies at c ^ f(r)
-    auto row_off = [&](int key) {
-        return (key >> p.box_shift) * (box * D * S::ESZ) + (key & (box - 1)) * S::ROWB;
-    };
-    auto swz = [&](int key) { return S::ROWB == 128 ? (key & 7) << 4 : ((key >> 1) & 3) << 4; };
-    const int span_b = box * S::ROWB;                              // bytes between the spans of a row
+    // key k's row begins at k * ROWB of a span, its 16-byte chunk c lies at c ^ f(k)
+    auto swz = [](int key) { return S::ROWB == 128 ? (key & 7) << 4 : ((key >> 1) & 3) << 4; };
+    // where this lane's rows of the matrix loads begin in K and V, and the swizzle of their columns
+    const int krow = F8 ? g : ((lane >> 4) << 3) + (lane & 7), vrow = (((lane >> 3) & 1) << 3) + (lane & 7);
+    const uint32_t k_at = krow * S::ROWB, v_at = vrow * S::ROWB;
+    const uint32_t k_x = F8 ? (8 * t) ^ swz(krow) : (((lane >> 3) & 1) << 4) ^ swz(krow), v_x = ((lane >> 4) << 4) ^ swz(vrow);
 
-    uint32_t chunk_no = wk;                                        // of this block, as the producer counts
-    while (left > 0) {
-        const int lo = cur.step, hi = static_cast<int>(min(static_cast<long long>(cur.steps), lo + left));
+    // ---- loads, by the group's first warp
+    const int box = 1 << p.box_shift, pieces = CK >> p.box_shift, batch = 32 / pieces;
+    auto chunks_of = [&](const Cursor& c, int from, int to) {
+        Chunks k;
+        k.table = a.c.page_table + static_cast<size_t>(c.b) * a.c.max_pages;
+        k.b = c.b;
+        k.h = c.h;
+        k.first = (from * WK + wk) * CK;
+        k.keys = tile_keys(a, c.s, c.mt, M);
+        const int stop = min(to * S::SK, k.keys);
+        k.n = stop > k.first ? (stop - k.first + S::SK - 1) / S::SK : 0;
+        return k;
+    };
+    // lane l has the page of piece l % pieces of chunk from + l / pieces
+    auto fetch = [&](const Chunks& k, int from) {
+        const int i = pieces == 1 ? from + lane : from + (lane >> 1);
+        const int key = k.first + i * S::SK + (pieces == 1 ? 0 : (lane & 1) * box);
+        return i < k.n && key < k.keys ? k.table[key >> a.c.page_shift] : -1;
+    };
+    int page_now = -1, page_next = -1, page_from = 0;              // of chunks page_from .. and the batch behind it
+    uint32_t done = 0;                                             // chunks this group has finished
+    // what is loaded of a chunk: pages of its pieces (-1: none), first key, bytes
+    int pg[2] = {-1, -1}, at_key = 0;
+    auto pages_of = [&](const Chunks& k, int i) {
+        const int at = (i - page_from) * pieces;
+        const int from = at < 32 ? page_now : page_next;
+        at_key = k.first + i * S::SK;
+        pg[0] = __shfl_sync(0xFFFFFFFFu, from, at & 31);
+        if (static_cast<unsigned>(pg[0]) >= static_cast<unsigned>(a.c.num_pages)) {
+            pg[0] = -1;
+            if (lane == 0) report(a.status, MOE_ERR_DEVICE, k.b);
+        }
+        pg[1] = -1;
+        if (pieces == 2) {
+            pg[1] = __shfl_sync(0xFFFFFFFFu, from, (at + 1) & 31);
+            if (static_cast<unsigned>(pg[1]) >= static_cast<unsigned>(a.c.num_pages)) {
+                pg[1] = -1;
+                if (at_key + box < k.keys && lane == 0) report(a.status, MOE_ERR_DEVICE, k.b);
+            }
+        }
+    };
+    // K (or V) of the chunk that pages_of looked at, the group's count-th; its stage has been read
+    // once WM warps have freed it
+    auto load = [&](const Chunks& k, uint32_t count, bool is_v) {
+        if (lane == 0) {
+            const uint32_t st = count % NG;
+            bool ok = true;
+            if (WM > 1 && count >= NG)
+                ok = ptx::mbar_wait(is_v ? &vfree[wk][st] : &kfree[wk][st], ((count / NG) - 1) & 1u, abort_flag, p.wait_limit,
+                                    a.status, 1u);
+            if (!is_v) {
+                uint32_t v = ALL;
+                if (pieces == 2) v = (pg[0] >= 0 ? 0xFFFFu : 0u) | (pg[1] >= 0 ? 0xFFFF0000u : 0u);
+                else if (pg[0] < 0) v = 0;
+                const int rest = k.keys - at_key;                  // >= 1
+                if (rest < CK) v &= (1u << rest) - 1u;
+                valid[wk][st] = v;
+            }
+            uint64_t* bar = is_v ? &vfull[wk][st] : &kfull[wk][st];
+            if (ok) {
+                ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>((pg[0] >= 0) + (pg[1] >= 0)) * box * D * S::ESZ);
+                unsigned char* dst = mem + (2 * st + is_v) * S::KBYTES;
+                const int slot = at_key & ((1 << a.c.page_shift) - 1);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (pg[q] < 0) continue;
+#pragma unroll
+                    for (int sp = 0; sp < S::SPANS; ++sp)          // (a second piece is a page of its own)
+                        ptx::tma_load_5d(dst + q * (CK / 2) * S::ROWB + sp * S::SPAN, is_v ? &p.tv : &p.tk, bar, 0, q ? 0 : slot, sp,
+                                         k.h, pg[q]);
+                }
+            }
+        }
+        __syncwarp();
+    };
+    auto begin = [&](const Chunks& k) {
+        page_from = 0;
+        page_now = fetch(k, 0);
+        page_next = k.n > batch ? fetch(k, batch) : -1;
+        for (int i = 0; i < NG && i < k.n; ++i) {
+            pages_of(k, i);
+            load(k, done + i, false);
+            load(k, done + i, true);
+        }
+    };
+    Chunks ch = chunks_of(cur, lo, hi);
+    if (leads) begin(ch);
+
+    while (true) {
         const SeqInfo s = cur.s;
         const int rows = s.n * a.group;
-        const int keys = tile_keys(a, s, cur.mt, M);
+        const int keys = ch.keys;
         const int r0 = cur.mt * M + wm * 16 + g;                   // this thread's rows: r0, r0 + 8
-        const int i0 = min(r0, rows - 1) / a.group, i1 = min(r0 + 8, rows - 1) / a.group;
+        const int i0 = token_of(a, min(r0, rows - 1)), i1 = token_of(a, min(r0 + 8, rows - 1));
 
-        // ---- Q as the first product's A operand
-        uint32_t qf[D / 16][4];
-        float sc0 = scale, sc1 = scale;
+        // ---- Q to shared memory: D / 8 lanes per row, 16 bytes each; rows behind the last are 0
         {
+            constexpr int LPR = D / 8, RPI = NW * 32 / LPR;
             const uint32_t sign = flip ? 0x80008000u : 0u;
-            const uint16_t* q0 = a.q + (s.row0 + i0) * a.q_stride + static_cast<long long>(cur.h * a.group + min(r0, rows - 1) % a.group) * D;
-            const uint16_t* q1 = a.q + (s.row0 + i1) * a.q_stride + static_cast<long long>(cur.h * a.group + min(r0 + 8, rows - 1) % a.group) * D;
-            const bool v0 = r0 < rows, v1 = r0 + 8 < rows;
-            if constexpr (!F8) {
+            const int ch = threadIdx.x % LPR;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
+            for (int r = threadIdx.x / LPR; r < (M + RPI - 1) / RPI * RPI; r += RPI) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                const int rr = cur.mt * M + r;
+                if (r < M && rr < rows) {
+                    const int i = token_of(a, rr);
+                    v = *reinterpret_cast<const uint4*>(a.q + (s.row0 + i) * a.q_stride +
+                                                        static_cast<long long>(cur.h * a.group + rr - i * a.group) * D + ch * 8);
+                    v.x ^= sign; v.y ^= sign; v.z ^= sign; v.w ^= sign;
+                }
+                if constexpr (!F8) {
+                    if (r < M) *reinterpret_cast<uint4*>(q_smem + r * S::QPITCH + ch * 16) = v;
+                } else {
+                    // a power of two brings the row to fp16; dimensions 32 blk + 8 t + 4 step +
+                    // {0, 1 | 2, 3} stand for k = 2t, 2t+1 | 2t+8, 2t+9 of step 2 blk + step
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    float mx = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int d = k * 16 + e * 8 + 2 * t;
-                        qf[k][2 * e] = v0 ? *reinterpret_cast<const uint32_t*>(q0 + d) ^ sign : 0u;
-                        qf[k][2 * e + 1] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + d) ^ sign : 0u;
+                    for (int j = 0; j < 4; ++j) {
+                        const float x = fabsf(__uint_as_float(w[j] << 16)), y = fabsf(__uint_as_float(w[j] & 0xFFFF0000u));
+                        mx = x < INFINITY ? fmaxf(mx, x) : mx;
+                        mx = y < INFINITY ? fmaxf(mx, y) : mx;
+                    }
+#pragma unroll
+                    for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                    const int e = f16_chunk_exp(mx);
+                    const float d = exp2_int(-e);
+                    if (r < M) {
+                        unsigned char* dst = q_smem + r * S::QPITCH + (ch >> 2) * 64 + (ch & 3) * 4;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint32_t*>(dst + (j >> 1) * 32 + (j & 1) * 16) =
+                                pack_f16x2(__uint_as_float(w[j] << 16) * d, __uint_as_float(w[j] & 0xFFFF0000u) * d);
+                        if (ch == 0) q_scale[r] = scale * exp2_int(e);
                     }
                 }
-            } else {
-                // dimensions 32 blk + 8 t + 4 step + {0, 1 | 2, 3} stand for k = 2t, 2t+1 | 2t+8, 2t+9
-                float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-                for (int blk = 0; blk < D / 32; ++blk) {
-                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                    if (v0) x = *reinterpret_cast<const uint4*>(q0 + blk * 32 + 8 * t);
-                    if (v1) y = *reinterpret_cast<const uint4*>(q1 + blk * 32 + 8 * t);
-                    qf[2 * blk][0] = x.x ^ sign; qf[2 * blk][2] = x.y ^ sign;
-                    qf[2 * blk + 1][0] = x.z ^ sign; qf[2 * blk + 1][2] = x.w ^ sign;
-                    qf[2 * blk][1] = y.x ^ sign; qf[2 * blk][3] = y.y ^ sign;
-                    qf[2 * blk + 1][1] = y.z ^ sign; qf[2 * blk + 1][3] = y.w ^ sign;
-                }
-                auto amax = [](float m, uint32_t w) {
-                    const float u = fabsf(__uint_as_float(w << 16)), v = fabsf(__uint_as_float(w & 0xFFFF0000u));
-                    m = u < INFINITY ? fmaxf(m, u) : m;
-                    return v < INFINITY ? fmaxf(m, v) : m;
-                };
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    m0 = amax(amax(m0, qf[k][0]), qf[k][2]);
-                    m1 = amax(amax(m1, qf[k][1]), qf[k][3]);
-                }
-#pragma unroll
-                for (int o = 1; o < 4; o <<= 1) {
-                    m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
-                    m1 = fmaxf(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, o));
-                }
-                const int e0 = f16_chunk_exp(m0), e1 = f16_chunk_exp(m1);
-                const float d0 = exp2_int(-e0), d1 = exp2_int(-e1);
-                sc0 *= exp2_int(e0);
-                sc1 *= exp2_int(e1);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float d = (e & 1) ? d1 : d0;
-                        qf[k][e] = pack_f16x2(__uint_as_float(qf[k][e] << 16) * d,
-                                              __uint_as_float(qf[k][e] & 0xFFFF0000u) * d);
-                    }
             }
+        }
+        compute_sync();
+        const uint32_t qa = ptx::smem_u32(q_smem) + (wm * 16 + (lane & 15)) * S::QPITCH + (lane >> 4) * 16;
+        float sc0 = scale, sc1 = scale;
+        if constexpr (F8) {
+            sc0 = q_scale[wm * 16 + g];
+            sc1 = q_scale[wm * 16 + g + 8];
         }
 
         float o[D / 8][4];
@@ -294,66 +315,71 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
             for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
+        constexpr int NT = CK / 8;                                 // key tiles of a chunk
         bool ok = true;
-        for (int st = lo; st < hi; ++st, chunk_no += WK) {
-            const int stage = chunk_no % NS;
-            ok = ptx::mbar_wait(&full[stage], (chunk_no / NS) & 1u, abort_flag, p.wait_limit, a.status, 2u);
+        for (int k = 0; k < ch.n; ++k, ++done) {
+            const uint32_t stage = done % NG, par = (done / NG) & 1u;
+            ok = ptx::mbar_wait(&kfull[wk][stage], par, abort_flag, p.wait_limit, a.status, 2u);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
-            const uint32_t vm = valid[stage];
-            const int c0 = (st * WK + wk) * CK;
-            if (vm != 0) {
-                const uint32_t kb = ring_u + stage * S::STAGE, vb = kb + S::KBYTES;
-                float sacc[4][4];
+            const uint32_t vm = valid[wk][stage];
+            const int c0 = ch.first + k * S::SK;
+            {
+                const uint32_t kb = mem_u + 2 * stage * S::KBYTES, vb = kb + S::KBYTES;
+                float sacc[NT][4];
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sacc[n][e] = 0.f;
                 if constexpr (!F8) {
-                    const int krow = ((lane >> 4) << 3) + (lane & 7), kcol = ((lane >> 3) & 1) << 4;
-                    const uint32_t ka0 = kb + row_off(krow), ka1 = kb + row_off(krow + 16);
-                    const int x = swz(krow);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const int col = ((k & 3) * 32 + kcol) ^ x;
-                        const uint32_t off = (k >> 2) * span_b + col;
-                        uint32_t r[4];
-                        ldsm4(r, ka0 + off);
-                        mma16816<false>(sacc[0], qf[k], r[0], r[1]);
-                        mma16816<false>(sacc[1], qf[k], r[2], r[3]);
-                        ldsm4(r, ka1 + off);
-                        mma16816<false>(sacc[2], qf[k], r[0], r[1]);
-                        mma16816<false>(sacc[3], qf[k], r[2], r[3]);
+                    for (int d = 0; d < D / 16; ++d) {
+                        const uint32_t at = kb + k_at + (d >> 2) * S::SPAN + (((d & 3) * 32) ^ k_x);
+                        uint32_t q[4], r[NT / 2][4];
+                        ldsm4(q, qa + d * 32);
+#pragma unroll
+                        for (int n = 0; n < NT / 2; ++n) ldsm4(r[n], at + n * 16 * S::ROWB);
+#pragma unroll
+                        for (int n = 0; n < NT / 2; ++n) {
+                            mma16816<false>(sacc[2 * n], q, r[n][0], r[n][1]);
+                            mma16816<false>(sacc[2 * n + 1], q, r[n][2], r[n][3]);
+                        }
                     }
                 } else {
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const int key = n * 8 + g;
-                        const uint32_t ka = kb + row_off(key);
-                        const int x = swz(key);
+                    for (int blk = 0; blk < D / 32; ++blk) {
+                        uint32_t q0[4], q1[4];
+                        ldsm4(q0, qa + blk * 64);
+                        ldsm4(q1, qa + blk * 64 + 32);
+                        const uint32_t at = kb + k_at + (blk * 32 / S::ROWB) * S::SPAN + ((blk * 32 % S::ROWB) ^ k_x);
+                        uint32_t w0[NT], w1[NT];
 #pragma unroll
-                        for (int blk = 0; blk < D / 32; ++blk) {
-                            const int byte = blk * 32 + 8 * t;
-                            const uint32_t off = (byte / S::ROWB) * span_b + ((byte % S::ROWB) ^ x);
-                            uint32_t w0, w1;
-                            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(ka + off) : "memory");
-                            mma16816<true>(sacc[n], qf[2 * blk], e4m3x2_to_f16x2(w0), e4m3x2_to_f16x2(w0 >> 16));
-                            mma16816<true>(sacc[n], qf[2 * blk + 1], e4m3x2_to_f16x2(w1), e4m3x2_to_f16x2(w1 >> 16));
+                        for (int n = 0; n < NT; ++n) {
+                            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                         : "=r"(w0[n]), "=r"(w1[n])
+                                         : "r"(at + n * 8 * S::ROWB)
+                                         : "memory");
                         }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma16816<true>(sacc[n], q0, e4m3x2_to_f16x2(w0[n]), e4m3x2_to_f16x2(w0[n] >> 16));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma16816<true>(sacc[n], q1, e4m3x2_to_f16x2(w1[n]), e4m3x2_to_f16x2(w1[n] >> 16));
                     }
                 }
                 // ---- scores in base 2, what a row does not see at -infinity
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
+                for (int n = 0; n < NT; ++n) {
                     sacc[n][0] *= sc0;
                     sacc[n][1] *= sc0;
                     sacc[n][2] *= sc1;
                     sacc[n][3] *= sc1;
                 }
-                if (vm != 0xFFFFFFFFu || c0 + CK > s.ctx) {
+                if (vm != ALL || c0 + CK > s.ctx) {
                     const uint32_t see0 = seen_bits(a, s, i0, c0, keys) & vm, see1 = seen_bits(a, s, i1, c0, keys) & vm;
 #pragma unroll
-                    for (int n = 0; n < 4; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int bit = n * 8 + 2 * t + e;
@@ -363,7 +389,7 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                 }
                 float x0m = fmaxf(sacc[0][0], sacc[0][1]), x1m = fmaxf(sacc[0][2], sacc[0][3]);
 #pragma unroll
-                for (int n = 1; n < 4; ++n) {
+                for (int n = 1; n < NT; ++n) {
                     x0m = fmaxf(x0m, fmaxf(sacc[n][0], sacc[n][1]));
                     x1m = fmaxf(x1m, fmaxf(sacc[n][2], sacc[n][3]));
                 }
@@ -371,6 +397,15 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                 for (int off = 1; off < 4; off <<= 1) {
                     x0m = fmaxf(x0m, __shfl_xor_sync(0xFFFFFFFFu, x0m, off));
                     x1m = fmaxf(x1m, __shfl_xor_sync(0xFFFFFFFFu, x1m, off));
+                }
+                // K has been read: the next one
+                if constexpr (WM > 1) {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&kfree[wk][stage]);
+                }
+                if (leads && k + NG < ch.n) {
+                    pages_of(ch, k + NG);
+                    load(ch, done + NG, false);
                 }
                 const bool up0 = x0m > m0 + 8.f || (m0 == -INFINITY && x0m > m0);
                 const bool up1 = x1m > m1 + 8.f || (m1 == -INFINITY && x1m > m1);
@@ -391,7 +426,7 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                 }
                 const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
+                for (int n = 0; n < NT; ++n) {
                     sacc[n][0] = ex2(sacc[n][0] - ref0);
                     sacc[n][1] = ex2(sacc[n][1] - ref0);
                     sacc[n][2] = ex2(sacc[n][2] - ref1);
@@ -400,10 +435,11 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                     l1 += sacc[n][2] + sacc[n][3];
                 }
                 // ---- O += P V
-                const int vrow = (((lane >> 3) & 1) << 3) + (lane & 7), vcol = (lane >> 4) << 4;
-                const int xv = swz(vrow);
+                ok = ptx::mbar_wait(&vfull[wk][stage], par, abort_flag, p.wait_limit, a.status, 3u);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
 #pragma unroll
-                for (int kp = 0; kp < 2; ++kp) {
+                for (int kp = 0; kp < CK / 16; ++kp) {
                     uint32_t pf[4];
                     if constexpr (F8) {
                         pf[0] = pack_f16x2(sacc[2 * kp][0], sacc[2 * kp][1]);
@@ -420,13 +456,13 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                     const uint32_t vk = vm >> (kp * 16 + 2 * t);
                     const uint32_t keep0 = ((vk & 1) ? 0xFFFFu : 0u) | ((vk & 2) ? 0xFFFF0000u : 0u);
                     const uint32_t keep1 = ((vk & 256) ? 0xFFFFu : 0u) | ((vk & 512) ? 0xFFFF0000u : 0u);
-                    const uint32_t va = vb + row_off(kp * 16 + vrow);
+                    const uint32_t va = vb + v_at + kp * 16 * S::ROWB;
                     if constexpr (!F8) {
 #pragma unroll
                         for (int n = 0; n < D / 16; ++n) {
                             uint32_t r[4];
-                            ldsm4_t(r, va + (n >> 2) * span_b + (((n & 3) * 32 + vcol) ^ xv));
-                            if (vm != 0xFFFFFFFFu) {
+                            ldsm4_t(r, va + (n >> 2) * S::SPAN + (((n & 3) * 32) ^ v_x));
+                            if (vm != ALL) {
                                 r[0] &= keep0; r[1] &= keep1; r[2] &= keep0; r[3] &= keep1;
                             }
                             mma16816<false>(o[2 * n], pf, r[0], r[1]);
@@ -435,10 +471,9 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                     } else {
 #pragma unroll
                         for (int blk = 0; blk < D / 32; ++blk) {
-                            const int byte = blk * 32;
                             uint32_t r[4];
-                            ldsm4_t(r, va + (byte / S::ROWB) * span_b + (((byte % S::ROWB) + vcol) ^ xv));
-                            if (vm != 0xFFFFFFFFu) {
+                            ldsm4_t(r, va + (blk * 32 / S::ROWB) * S::SPAN + ((blk * 32 % S::ROWB) ^ v_x));
+                            if (vm != ALL) {
                                 r[0] &= keep0; r[1] &= keep1; r[2] &= keep0; r[3] &= keep1;
                             }
 #pragma unroll
@@ -452,7 +487,27 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                 }
             }
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&empty[stage]);
+            if constexpr (WM > 1) {
+                if (lane == 0) ptx::mbar_arrive(&vfree[wk][stage]);
+            }
+            if (leads) {
+                if (k + NG < ch.n) load(ch, done + NG, true);
+                if (k + 1 - page_from >= batch) {
+                    page_from += batch;
+                    page_now = page_next;
+                    page_next = fetch(ch, page_from + batch);
+                }
+            }
+        }
+        // the next item's first chunks are on their way while this one's results are joined
+        Cursor nxt = cur;
+        Chunks nch = ch;
+        long long nleft = left;
+        int nlo = 0, nhi = 0;
+        const bool more = ok && nxt.segment(a, G, nleft, nlo, nhi);
+        if (more) {
+            nch = chunks_of(nxt, nlo, nhi);
+            if (leads) begin(nch);
         }
 
         // ---- the warps' results meet in shared memory
@@ -461,50 +516,86 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
             l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, off);
             l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, off);
         }
-        const int br = wk * M + wm * 16 + g;                       // row of the merge buffer
-        if (t == 0) {
-            ml[br][0] = m0;
-            ml[br][1] = l0;
-            ml[br + 8][0] = m1;
-            ml[br + 8][1] = l1;
-        }
+        constexpr int HK = WK / 2;
+        auto spot = [&](int e, int n) {                            // this thread's places in rows g + 8e of its group's part
+            float* dst = buf + ((wk % HK) * M + wm * 16 + g + 8 * e) * S::PITCH;
+            return F8 ? dst + n * 16 + 4 * t : dst + n * 8 + 2 * t;
+        };
+        const int br = (wk % HK) * M + wm * 16 + g;
+        compute_sync();                                            // Q has been read
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float* dst = buf + (br + 8 * e) * S::PITCH;
-            if constexpr (!F8) {
+        for (int round = 0; round < 2; ++round) {
+            // the upper half of the groups leaves its results, the lower half adds its own
+            if (round == 1) compute_sync();
+            if ((round == 0) != (wk >= HK)) continue;
+            float f0 = 1.f, f1 = 1.f, g0 = 0.f, g1 = 0.f;
+            if (round == 1) {
+                const float2 a0 = *reinterpret_cast<const float2*>(ml[br]), a1 = *reinterpret_cast<const float2*>(ml[br + 8]);
+                const float n0 = fmaxf(m0, a0.x), n1 = fmaxf(m1, a1.x);
+                const float ref0 = n0 == -INFINITY ? 0.f : n0, ref1 = n1 == -INFINITY ? 0.f : n1;
+                f0 = ex2(m0 - ref0);
+                f1 = ex2(m1 - ref1);
+                g0 = ex2(a0.x - ref0);
+                g1 = ex2(a1.x - ref1);
+                m0 = n0;
+                m1 = n1;
+                l0 = l0 * f0 + a0.y * g0;
+                l1 = l1 * f1 + a1.y * g1;
+                __syncwarp();                                      // (the quad has read its row's statistics)
+            }
+            if (t == 0) {
+                *reinterpret_cast<float2*>(ml[br]) = make_float2(m0, l0);
+                *reinterpret_cast<float2*>(ml[br + 8]) = make_float2(m1, l1);
+            }
 #pragma unroll
-                for (int n = 0; n < D / 8; ++n)
-                    *reinterpret_cast<float2*>(dst + n * 8 + 2 * t) = make_float2(o[n][2 * e], o[n][2 * e + 1]);
-            } else {
+            for (int e = 0; e < 2; ++e) {
+                const float f = e ? f1 : f0, gg = e ? g1 : g0;
+                if constexpr (!F8) {
 #pragma unroll
-                for (int n = 0; n < D / 16; ++n)
-                    *reinterpret_cast<float4*>(dst + n * 16 + 4 * t) =
-                        make_float4(o[2 * n][2 * e], o[2 * n + 1][2 * e], o[2 * n][2 * e + 1], o[2 * n + 1][2 * e + 1]);
+                    for (int n = 0; n < D / 8; ++n) {
+                        float2* at = reinterpret_cast<float2*>(spot(e, n));
+                        float2 v = make_float2(o[n][2 * e], o[n][2 * e + 1]);
+                        if (round == 1) {
+                            const float2 u = *at;
+                            v = make_float2(v.x * f + u.x * gg, v.y * f + u.y * gg);
+                        }
+                        *at = v;
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < D / 16; ++n) {
+                        float4* at = reinterpret_cast<float4*>(spot(e, n));
+                        float4 v = make_float4(o[2 * n][2 * e], o[2 * n + 1][2 * e], o[2 * n][2 * e + 1], o[2 * n + 1][2 * e + 1]);
+                        if (round == 1) {
+                            const float4 u = *at;
+                            v = make_float4(v.x * f + u.x * gg, v.y * f + u.y * gg, v.z * f + u.z * gg, v.w * f + u.w * gg);
+                        }
+                        *at = v;
+                    }
+                }
             }
         }
         compute_sync();
         const bool whole = lo == 0 && hi == cur.steps;
         const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (lo == 0);
-        if (threadIdx.x == 0 && lo == 0 && !whole)                 // (the last of the share, so left == hi)
-            p.part.items[blockIdx.x] = JoinItem{parts_until(W, shares, blockIdx.x, x1 - hi + cur.steps), s.row0, rows, cur.h, cur.mt};
-        for (int r = warp; r < M; r += 4) {
+        for (int r = warp; r < M; r += NW) {
             const int rr = cur.mt * M + r;
             if (rr >= rows) break;
             float m = ml[r][0];
 #pragma unroll
-            for (int w = 1; w < WK; ++w) m = fmaxf(m, ml[w * M + r][0]);
+            for (int w = 1; w < HK; ++w) m = fmaxf(m, ml[w * M + r][0]);
             float l = 0.f, acc[EPL];
 #pragma unroll
             for (int j = 0; j < EPL; ++j) acc[j] = 0.f;
             const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int w = 0; w < WK; ++w) {
+            for (int w = 0; w < HK; ++w) {
                 const float f = ex2(ml[w * M + r][0] - ref);
                 l += ml[w * M + r][1] * f;
 #pragma unroll
                 for (int j = 0; j < EPL; ++j) acc[j] += buf[(w * M + r) * S::PITCH + lane * EPL + j] * f;
             }
-            const int i = rr / a.group, head = cur.h * a.group + rr % a.group;
+            const int i = token_of(a, rr), head = cur.h * a.group + rr - i * a.group;
             const long long row = s.row0 + i;
             bool nan = false;
 #pragma unroll
@@ -540,12 +631,42 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                 if (lane == 0) *reinterpret_cast<float2*>(p.part.ml + (slot * M + r) * 2) = make_float2(m, l);
             }
         }
+        if (!whole) {
+            // the last block to leave its part of the item joins them
+            const int2 in = item_shares(shares, cur, G, x1, left);
+            __threadfence();
+            compute_sync();
+            if (threadIdx.x == 0) {
+                const bool last = atomicAdd(p.part.arrived + in.x, 1u) == static_cast<unsigned>(in.y) - 1u;
+                if (last) p.part.arrived[in.x] = 0;
+                s_last = last;
+            }
+            compute_sync();
+            if (s_last) {
+                __threadfence();
+                for (int r = warp; r < M && cur.mt * M + r < rows; r += NW)
+                    join_row<EPL>(a, p.part, M, in.x, in.y, s.row0, cur.h, r, cur.mt * M + r, lane);
+            }
+        }
         // after a wait that ran out every warp leaves here, at the same item
         if (threadIdx.x == 0) s_stop = *abort_flag;
         compute_sync();                                            // (and the merge buffer is free)
-        if (s_stop) break;
-        left -= hi - lo;
-        if (left > 0) cur.next(a, G);
+        if (s_stop || !more) break;
+        cur = nxt;
+        ch = nch;
+        left = nleft;
+        lo = nlo;
+        hi = nhi;
+    }
+    if (s_stop && leads && lane == 0) {
+        // loads in flight land before the block's memory goes away: the last use of each stage, if
+        // it was not waited for, is the one `done` or the one NG - 1 chunks behind it at most
+        for (uint32_t i = done; i < done + NG; ++i) {
+            const long long t0 = clock64();
+            while (!(ptx::mbar_try_wait(&kfull[wk][i % NG], (i / NG) & 1u) && ptx::mbar_try_wait(&vfull[wk][i % NG], (i / NG) & 1u)) &&
+                   clock64() - t0 < (1ll << 24)) {
+            }
+        }
     }
 }
 
@@ -555,11 +676,10 @@ cudaError_t launch_cfg(const AttnArgs& a, void* partials, int sms, cudaStream_t 
     SmallParams p;
     p.a = a;
     const int page = 1 << a.c.page_shift;
-    const int box = page < CK ? page : CK;
-    p.box_shift = page < CK ? a.c.page_shift : 5;
-    p.least = 2;
+    const int box = page < S::CK ? page : S::CK;
+    p.box_shift = page < S::CK ? a.c.page_shift : (S::CK == 32 ? 5 : 4);
     p.wait_limit = 4ll << 30;
-    if (!make_kv_map(&p.tk, a, false, box, true) || !make_kv_map(&p.tv, a, true, box, true)) return cudaErrorInvalidValue;
+    if (!make_kv_map(&p.tk, a, false, box) || !make_kv_map(&p.tv, a, true, box)) return cudaErrorInvalidValue;
     const int blocks = sms * S::BLOCKS_PER_SM < kSmallBlocks ? sms * S::BLOCKS_PER_SM : kSmallBlocks;
     p.part = partials_at(partials, blocks, S::M);
     const cudaError_t e = cudaFuncSetAttribute(small_kernel<D, F8, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
@@ -571,7 +691,7 @@ cudaError_t launch_cfg(const AttnArgs& a, void* partials, int sms, cudaStream_t 
     }
     const cudaError_t le = cudaGetLastError();
     if (le != cudaSuccess) return le;
-    return launch_tree_attn_join(a, S::M, p.part, blocks, st);
+    return cudaSuccess;
 }
 
 template <int D, bool F8>

@@ -23,6 +23,7 @@ namespace {
 
 constexpr int TK = 128;                  // keys per step
 constexpr int TL_THREADS = 320;
+constexpr int kTileExtra = 2;            // what an item costs besides its steps, in steps
 constexpr int kInfo = 8;                 // steps whose key masks are kept (the producer is at most 6 ahead)
 
 template <int D>
@@ -40,7 +41,6 @@ struct TileParams {
     CUtensorMap tk, tv;
     Partials part;
     int box_shift;
-    int least;
     long long wait_limit;
 };
 
@@ -83,7 +83,7 @@ template <int D>
 __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_constant__ TileParams p) {
     using S = Tile<D>;
     constexpr int NS = S::NS;
-    constexpr Tiling G{kTileRows, TK};
+    constexpr Tiling G{kTileRows, TK, kTileExtra};
     extern __shared__ __align__(1024) unsigned char tl_raw[];
     __shared__ ScanShared scan;
     __shared__ uint64_t full[NS], empty[NS], q_ready[2], s_full[2], p_ready[2], o_full[2], tail_bar, drain_bar;
@@ -115,13 +115,14 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
     }
     long long before;
     int b0, b1;
-    const long long W = scan_steps(a, G, scan, &before, &b0, &b1);
-    const int shares = W > 0 ? share_count(W, gridDim.x, p.least) : 0;
+    const long long W = scan_units(a, G, scan, &before, &b0, &b1);
+    const Shares shares(W, gridDim.x, 4 + kTileExtra);
     if (threadIdx.x == 0) p.part.items[blockIdx.x].parts = 0;
-    if (static_cast<int>(blockIdx.x) >= shares) return;
-    const long long x0 = share_begin(W, blockIdx.x, shares), x1 = share_begin(W, blockIdx.x + 1, shares);
+    if (static_cast<int>(blockIdx.x) >= shares.count) return;
+    const long long x0 = shares.begin(blockIdx.x), x1 = shares.begin(blockIdx.x + 1);
     Cursor cur = seek(a, G, scan, x0, before, b0, b1);
     long long left = x1 - x0;
+    int lo, hi;
     if (warp == 8) {
         ptx::tmem_alloc(&tmem_base_s, 512);
         ptx::tmem_relinquish();
@@ -136,8 +137,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
         const int box = 1 << p.box_shift, pieces = TK >> p.box_shift;
         uint32_t n = 0, step_no = 0, tail_phase = 0;               // slots and steps so far
         bool ok = true;
-        while (left > 0 && ok) {
-            const int lo = cur.step, hi = static_cast<int>(min(static_cast<long long>(cur.steps), lo + left));
+        while (ok && cur.segment(a, G, left, lo, hi)) {
             const int keys = tile_keys(a, cur.s, cur.mt, G.M);
             const int32_t* table = a.c.page_table + static_cast<size_t>(cur.b) * a.c.max_pages;
             const int first = lo * TK, stop = min(hi * TK, keys);
@@ -214,8 +214,6 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                     }
                 }
             }
-            left -= hi - lo;
-            if (left > 0) cur.next(a, G);
         }
         if (lane == 0 && *abort_flag) {
             // every copy in flight lands before the block's memory goes away
@@ -254,8 +252,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                     ptx::mma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8, ptx::smem_desc_mn128(va + k * 2048, S::SPAN), IO,
                                     add || k != 0);
             };
-            while (left > 0 && ok) {
-                const int lo = cur.step, hi = static_cast<int>(min(static_cast<long long>(cur.steps), lo + left));
+            while (ok && cur.segment(a, G, left, lo, hi)) {
                 const bool two = cur.s.n * a.group - cur.mt * G.M > 128;
                 if (!wait(&full[n % NS], (n / NS) & 1u, 3u)) break;
                 for (int h = 0; h < (two ? 2 : 1); ++h) {
@@ -290,8 +287,6 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                     }
                     if (!ok) break;
                 }
-                left -= hi - lo;
-                if (left > 0) cur.next(a, G);
             }
             // every product has finished before TMEM is freed
             ptx::mma_commit(&drain_bar);
@@ -308,8 +303,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
         const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;   // a negative scale: q changes sign instead
         uint32_t sp = 0, op = 0, step_no = 0;
         bool ok = true;
-        while (left > 0 && ok) {
-            const int lo = cur.step, hi = static_cast<int>(min(static_cast<long long>(cur.steps), lo + left));
+        while (ok && cur.segment(a, G, left, lo, hi)) {
             const SeqInfo s = cur.s;
             const int rows = s.n * a.group - cur.mt * G.M - h * 128;   // of this half
             if (rows > 0) {
@@ -324,7 +318,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                         const int r = sub * 32 + k * RPI + lane / LPR;
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (r < rows) {
-                            const int rr = r_first + r, i = rr / a.group;
+                            const int rr = r_first + r, i = token_of(a, rr);
                             v = *reinterpret_cast<const uint4*>(a.q + (s.row0 + i) * a.q_stride +
                                                                 static_cast<long long>(cur.h * a.group + rr - i * a.group) * D + ch * 8);
                             v.x ^= sign; v.y ^= sign; v.z ^= sign; v.w ^= sign;
@@ -336,9 +330,9 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                 }
                 const int keys = tile_keys(a, s, cur.mt, G.M);
                 const int rr = r_first + min(sub * 32 + lane, rows - 1);   // this thread's row (or the last one)
-                const int i = rr / a.group;
+                const int i = token_of(a, rr);
                 // steps that end in front of this key need no look at what a row sees
-                const int clear = a.mask != nullptr ? s.ctx : s.ctx + r_first / a.group + 1;
+                const int clear = a.mask != nullptr ? s.ctx : s.ctx + token_of(a, r_first) + 1;
                 float m = -INFINITY, l = 0.f;
                 for (int st = lo; st < hi; ++st, ++step_no) {
                     ok = ptx::mbar_wait(&s_full[h], sp, abort_flag, p.wait_limit, a.status, 6u);
@@ -429,7 +423,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                 const size_t slot_row = (2 * static_cast<size_t>(blockIdx.x) + (lo == 0)) * kTileRows + h * 128 + sub * 32 + lane;
                 if (threadIdx.x == 0 && lo == 0 && !whole)         // (the last of the share; half 0 always has rows)
                     p.part.items[blockIdx.x] =
-                        JoinItem{parts_until(W, shares, blockIdx.x, x1 - hi + cur.steps), s.row0, s.n * a.group, cur.h, cur.mt};
+                        JoinItem{item_shares(shares, cur, G, x1, left).y, s.row0, s.n * a.group, cur.h, cur.mt};
                 float* part_o = p.part.o + slot_row * D;
                 float* part_ml = p.part.ml + slot_row * 2;
                 const float inv = l == 0.f ? 0.f : a.c.v_scale / l;
@@ -483,8 +477,6 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
             } else {
                 step_no += hi - lo;
             }
-            left -= hi - lo;
-            if (left > 0) cur.next(a, G);
         }
     }
     __syncwarp();
@@ -504,9 +496,8 @@ cudaError_t launch_tiles(const AttnArgs& a, void* partials, int sms, cudaStream_
     const int page = 1 << a.c.page_shift;
     const int box = page < TK ? page : TK;
     p.box_shift = page < TK ? a.c.page_shift : 7;
-    p.least = 4;
     p.wait_limit = 16ll << 30;
-    if (!make_kv_map(&p.tk, a, false, box, false) || !make_kv_map(&p.tv, a, true, box, false)) return cudaErrorInvalidValue;
+    if (!make_kv_map(&p.tk, a, false, box) || !make_kv_map(&p.tv, a, true, box)) return cudaErrorInvalidValue;
     const int blocks = sms < kTileBlocks ? sms : kTileBlocks;
     p.part = partials_at(partials, blocks, kTileRows);
     const cudaError_t e = cudaFuncSetAttribute(tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
