@@ -224,27 +224,51 @@ def moe_quant_rows_e4m3(rows, cols, inp, codes, scales, stream=None):
 
 # ---- paged cache, tree attention, log probabilities
 
+# (the checks are written for speed: a decoding step calls these once per layer, and a
+# launch is shorter than a few dozen attribute look-ups)
+
 def _rows(name, t, dtype):
     """Row stride of a tensor whose rows are dense: [T, n] or [T, heads, d]."""
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    stride, shape = t.stride(), t.shape
     inner = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != inner:
+    for i in range(len(shape) - 1, 0, -1):
+        if stride[i] != inner and shape[i] != 1:
             raise ValueError(f"{name}: the rows of a [T, ...] tensor have to be dense")
-        inner *= size
-    return t.stride(0) if t.shape[0] > 1 else max(inner, t.stride(0))
+        inner *= shape[i]
+    return (stride[0] if shape[0] > 1 else max(inner, stride[0])), inner
 
 
-def _dense(name, t, dtype, shape=None):
-    if t is None:
-        return
+def _dense(name, t, dtype, shape):
+    """Address of a contiguous tensor of that type and shape (None: any shape)."""
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, not {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} has to be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}, not {shape}")
+    return t.data_ptr()
+
+
+def _launch(name, fn, t, stream, *args):
+    """Calls an entry point on `stream` (None: the current one) with t's device current."""
+    at = t.device.index
+    if at is None or at == _current_device():
+        rc = fn(*args, _raw_stream(at) if stream is None and at is not None else _stream(stream))
+    else:
+        with torch.cuda.device(at):
+            rc = fn(*args, _stream(stream))
+    if rc != MOE_OK:
+        raise MoeError(name, rc)
+
+
+def _current_device():
+    return torch.cuda.current_device()
+
+
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def make_kv_cache(k, v, k_scale: float = 1.0, v_scale: float = 1.0) -> moe_kv_cache:
@@ -276,44 +300,27 @@ def make_kv_batch(q_start, ctx_len, page_table, max_new: int) -> moe_kv_batch:
     return b
 
 
-class _on:
-    """The device of `t` made current for a launch (streams belong to a device)."""
-
-    def __init__(self, t):
-        at = t.device.index
-        self.guard = None if at is None or at == torch.cuda.current_device() else torch.cuda.device(at)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
 def moe_qk_norm_rope_append(cache, batch, n_q: int, rot: int, eps: float, qkv, positions, q_norm_w, k_norm_w, cos_sin,
                             q_out, bad_tokens=None, stream=None):
     """qkv [T, (n_q + 2 n_kv) d] bf16 -> q_out [T, n_q d] bf16 and the cache (see
     include/moe.h); q_norm_w / k_norm_w None: no norm, rot 0: no rotation."""
     d, T = cache.head_dim, qkv.shape[0]
-    qs, os_ = _rows("qkv", qkv, torch.bfloat16), _rows("q_out", q_out, torch.bfloat16)
-    if qkv[:1].numel() not in (0, (n_q + 2 * cache.n_kv) * d) or q_out.shape[0] != T or \
-            q_out[:1].numel() not in (0, n_q * d, (n_q + 2 * cache.n_kv) * d):
+    bf16 = torch.bfloat16
+    qs, qn = _rows("qkv", qkv, bf16)
+    os_, on = _rows("q_out", q_out, bf16)
+    width = (n_q + 2 * cache.n_kv) * d
+    if qn != width or q_out.shape[0] != T or (on != n_q * d and on != width):
         raise ValueError("qkv [T, (n_q + 2 n_kv) d] and q_out [T, n_q d]")
-    _dense("q_norm_w", q_norm_w, torch.bfloat16, (d,))
-    _dense("k_norm_w", k_norm_w, torch.bfloat16, (d,))
-    _dense("bad_tokens", bad_tokens, torch.int32)
-    max_pos = 0
+    qw = None if q_norm_w is None else _dense("q_norm_w", q_norm_w, bf16, (d,))
+    kw = None if k_norm_w is None else _dense("k_norm_w", k_norm_w, bf16, (d,))
+    bad = None if bad_tokens is None else _dense("bad_tokens", bad_tokens, torch.int32, None)
+    max_pos, pos, cs = 0, None, None
     if rot > 0:
-        _dense("positions", positions, torch.int32, (T,))
-        _dense("cos_sin", cos_sin, torch.float32, (cos_sin.shape[0], rot))
         max_pos = cos_sin.shape[0]
-    with _on(qkv):
-        _check("moe_qk_norm_rope_append", lib().moe_qk_norm_rope_append(
-            C.byref(cache), C.byref(batch), T, n_q, rot, eps, _p(qkv), qs, _p(positions if rot > 0 else None), max_pos,
-            _p(q_norm_w), _p(k_norm_w), _p(cos_sin if rot > 0 else None), _p(q_out), os_, _p(bad_tokens),
-            _stream(stream)))
+        pos = _dense("positions", positions, torch.int32, (T,))
+        cs = _dense("cos_sin", cos_sin, torch.float32, (max_pos, rot))
+    _launch("moe_qk_norm_rope_append", lib().moe_qk_norm_rope_append, qkv, stream, cache, batch, T, n_q, rot, eps,
+            qkv.data_ptr(), qs, pos, max_pos, qw, kw, cs, q_out.data_ptr(), os_, bad)
 
 
 def moe_tree_attention_workspace_size(cache, n_q: int, T: int) -> int:
@@ -337,53 +344,50 @@ def moe_tree_attention(cache, batch, n_q: int, q, out, ws, tree_mask=None, lse=N
     tree_mask [T, words] int64 (bit j: the row sees its sequence's new token j) or None
     for a chain; scale None: 1 / sqrt(head dim)."""
     T, d = q.shape[0], cache.head_dim
-    qs, os_ = _rows("q", q, torch.bfloat16), _rows("out", out, torch.bfloat16)
-    if out.shape[0] != T or q[:1].numel() not in (0, n_q * d) or out[:1].numel() not in (0, n_q * d):
+    qs, qn = _rows("q", q, torch.bfloat16)
+    os_, on = _rows("out", out, torch.bfloat16)
+    if out.shape[0] != T or qn != n_q * d or on != qn:
         raise ValueError("q and out: [T, n_q d]")
-    _dense("lse", lse, torch.float32, (T, n_q))
-    words = 0
+    ls = None if lse is None else _dense("lse", lse, torch.float32, (T, n_q))
+    words, mask = 0, None
     if tree_mask is not None:
         words = tree_mask.shape[1]
-        _dense("tree_mask", tree_mask, torch.int64, (T, words))
-    with _on(q):
-        _check("moe_tree_attention", lib().moe_tree_attention(
-            C.byref(cache), C.byref(batch), T, n_q, d ** -0.5 if scale is None else scale, _p(q), qs, _p(tree_mask), words,
-            _p(out), os_, _p(lse), _p(ws), ws.numel(), _stream(stream)))
+        mask = _dense("tree_mask", tree_mask, torch.int64, (T, words))
+    _launch("moe_tree_attention", lib().moe_tree_attention, q, stream, cache, batch, T, n_q,
+            d ** -0.5 if scale is None else scale, q.data_ptr(), qs, mask, words, out.data_ptr(), os_, ls, ws.data_ptr(),
+            ws.numel())
 
 
 def moe_kv_compact(cache, batch, accepted, n_accepted, n_layers: int = 1, layer_stride: int = 0, bad_seqs=None,
                    stream=None):
     """Moves accepted [B, max_accept] int32 new tokens' keys and values to the front of
     their sequences' new tokens, in place, in n_layers caches layer_stride elements apart."""
-    B = batch.B
-    _dense("accepted", accepted, torch.int32, (B, accepted.shape[1]))
-    _dense("n_accepted", n_accepted, torch.int32, (B,))
-    _dense("bad_seqs", bad_seqs, torch.int32)
-    with _on(accepted):
-        _check("moe_kv_compact", lib().moe_kv_compact(
-            C.byref(cache), C.byref(batch), n_layers, layer_stride, _p(accepted), accepted.shape[1], _p(n_accepted),
-            _p(bad_seqs), _stream(stream)))
+    B, most = batch.B, accepted.shape[1]
+    acc = _dense("accepted", accepted, torch.int32, (B, most))
+    n = _dense("n_accepted", n_accepted, torch.int32, (B,))
+    bad = None if bad_seqs is None else _dense("bad_seqs", bad_seqs, torch.int32, None)
+    _launch("moe_kv_compact", lib().moe_kv_compact, accepted, stream, cache, batch, n_layers, layer_stride, acc, most, n, bad)
 
 
 def moe_token_logprobs(logits, targets, logprobs, entropy=None, top_ids=None, top_logprobs=None, stream=None):
     """logits [T, V] (bf16 or fp32, dense rows) and targets [T] int32 -> logprobs [T],
     entropy [T], top_ids / top_logprobs [T, n], each fp32 (ids int32) or None."""
     T, V = logits.shape
-    dt = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}.get(logits.dtype)
-    if dt is None:
-        raise TypeError(f"logits are {logits.dtype}, not bf16 or fp32")
-    _dense("targets", targets, torch.int32, (T,))
-    _dense("logprobs", logprobs, torch.float32, (T,))
-    _dense("entropy", entropy, torch.float32, (T,))
-    n = 0
-    if top_ids is not None:
-        n = top_ids.shape[1]
-        _dense("top_ids", top_ids, torch.int32, (T, n))
-        _dense("top_logprobs", top_logprobs, torch.float32, (T, n))
-    with _on(logits):
-        _check("moe_token_logprobs", lib().moe_token_logprobs(
-            T, V, dt, _p(logits), _rows("logits", logits, logits.dtype), _p(targets), n, _p(logprobs), _p(entropy),
-            _p(top_ids if n else None), _p(top_logprobs if n else None), _stream(stream)))
+    dt = logits.dtype
+    code = MOE_BF16 if dt == torch.bfloat16 else MOE_F32 if dt == torch.float32 else None
+    if code is None:
+        raise TypeError(f"logits are {dt}, not bf16 or fp32")
+    f32 = torch.float32
+    tg = None if targets is None else _dense("targets", targets, torch.int32, (T,))
+    lp = None if logprobs is None else _dense("logprobs", logprobs, f32, (T,))
+    en = None if entropy is None else _dense("entropy", entropy, f32, (T,))
+    n = 0 if top_ids is None else top_ids.shape[1]
+    ids = top = None
+    if n:
+        ids = _dense("top_ids", top_ids, torch.int32, (T, n))
+        top = _dense("top_logprobs", top_logprobs, f32, (T, n))
+    _launch("moe_token_logprobs", lib().moe_token_logprobs, logits, stream, T, V, code, logits.data_ptr(),
+            _rows("logits", logits, dt)[0], tg, n, lp, en, ids, top)
 
 
 def moe_get_status(ws, stream=None) -> int:
