@@ -44,6 +44,24 @@ struct TileParams {
     long long wait_limit;
 };
 
+// pairs of fp32 in one register pair: one instruction for two multiply-adds or additions
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 __device__ __forceinline__ float tl_ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -178,7 +196,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                 const bool partial = __any_sync(0xFFFFFFFFu, lane < 4 && word != 0xFFFFFFFFu);
                 const uint32_t bytes = static_cast<uint32_t>(__popc(goods)) * box * 128u * S::SPANS;
                 const int slot_in_page = c & ((1 << a.c.page_shift) - 1);
-#pragma unroll
+#pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++n) {
                     const uint32_t sl = n % NS;
                     ok = ok && ptx::mbar_wait(&empty[sl], ((n / NS) & 1u) ^ 1u, abort_flag, p.wait_limit, a.status, 1u);
@@ -200,6 +218,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                         ok = ptx::mbar_wait(&tail_bar, tail_phase, abort_flag, p.wait_limit, a.status, 7u);
                         tail_phase ^= 1u;
                         ok = __all_sync(0xFFFFFFFFu, ok);
+#pragma unroll 1
                         for (int r = lane; r < TK; r += 32) {
                             const uint32_t w = __shfl_sync(0xFFFFFFFFu, word, r >> 5);
                             if (w >> (r & 31) & 1) continue;
@@ -237,24 +256,29 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                 ok = ok && ptx::mbar_wait(bar, par, abort_flag, p.wait_limit, a.status, site);
                 return ok;
             };
+            // descriptors differ in their start address alone (16-byte units in the low word)
+            const uint64_t d_k = ptx::smem_desc_sw<128>(0), d_mn = ptx::smem_desc_mn128(0, S::SPAN);
+            const uint32_t k_hi = static_cast<uint32_t>(d_k >> 32), k_lo = static_cast<uint32_t>(d_k);
+            const uint32_t mn_hi = static_cast<uint32_t>(d_mn >> 32), mn_lo = static_cast<uint32_t>(d_mn);
+            auto desc = [](uint32_t hi_w, uint32_t lo_w) { return static_cast<uint64_t>(hi_w) << 32 | lo_w; };
             auto scores = [&](int h, uint32_t kslot) {
-                const uint32_t ka = ring_u + kslot * S::SLOT, qa = q_u + h * S::QHALF;
+                const uint32_t ka = k_lo + ((ring_u + kslot * S::SLOT) >> 4), qa = k_lo + ((q_u + h * S::QHALF) >> 4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k >> 2) * S::SPAN + (k & 3) * 32;
-                    ptx::mma_f16(tmem + h * 128, ptx::smem_desc_sw<128>(qa + off), ptx::smem_desc_sw<128>(ka + off), IS, k != 0);
+                    const uint32_t off = ((k >> 2) * S::SPAN + (k & 3) * 32) >> 4;
+                    ptx::mma_f16(tmem + h * 128, desc(k_hi, qa + off), desc(k_hi, ka + off), IS, k != 0);
                 }
             };
             auto values = [&](int h, uint32_t vslot, bool add) {
-                const uint32_t va = ring_u + vslot * S::SLOT;
+                const uint32_t va = mn_lo + ((ring_u + vslot * S::SLOT) >> 4);
 #pragma unroll
                 for (int k = 0; k < TK / 16; ++k)
-                    ptx::mma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8, ptx::smem_desc_mn128(va + k * 2048, S::SPAN), IO,
-                                    add || k != 0);
+                    ptx::mma_f16_ts(tmem + 256 + h * 128, tmem + h * 128 + 64 + k * 8, desc(mn_hi, va + k * 128), IO, add || k != 0);
             };
             while (ok && cur.segment(a, G, left, lo, hi)) {
                 const bool two = cur.s.n * a.group - cur.mt * G.M > 128;
                 if (!wait(&full[n % NS], (n / NS) & 1u, 3u)) break;
+#pragma unroll 1
                 for (int h = 0; h < (two ? 2 : 1); ++h) {
                     if (!wait(&q_ready[h], qp[h], 4u)) break;
                     qp[h] ^= 1u;
@@ -268,7 +292,8 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                     const bool more = st + 1 < hi;
                     const uint32_t vn = n + 1, kn = n + 2;
                     if (!wait(&full[vn % NS], (vn / NS) & 1u, 3u)) break;
-                    for (int h = 0; h < (two ? 2 : 1); ++h) {
+    #pragma unroll 1
+                for (int h = 0; h < (two ? 2 : 1); ++h) {
                         if (!wait(&p_ready[h], pp[h], 5u)) break;
                         pp[h] ^= 1u;
                         ptx::tc_fence_after();
@@ -348,20 +373,38 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
 #pragma unroll
                         for (int q = 0; q < 4; ++q) see[q] = seen_bits(a, s, i, c0 + 32 * q, keys) & word[q];
                     }
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t x[32];
-                        ptx::tmem_ld_32x32b_x32(s_t + q * 32, x);
-                        ptx::tmem_ld_wait(x);
+                    // the maximum over keys 0..63, then over 64..127, which stay in registers
+                    uint32_t xa[2][32], xb[2][32];
+                    auto hide = [&](uint32_t (&x)[32], int q) {
                         if (masked) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 if (!(see[q] >> e & 1)) x[e] = 0xFF800000u;
                         }
+                    };
+                    auto largest = [&](const uint32_t (&x)[32]) {
+                        float u = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), v = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
-                    }
+                        for (int e = 4; e < 32; e += 4) {
+                            u = fmaxf(fmaxf(u, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+                            v = fmaxf(fmaxf(v, __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
+                        }
+                        return fmaxf(u, v);
+                    };
+                    ptx::tmem_ld_32x32b_x32(s_t, xa[0]);
+                    ptx::tmem_ld_32x32b_x32(s_t + 32, xa[1]);
+                    ptx::tmem_ld_wait(xa[0]);
+                    ptx::tmem_ld_wait(xa[1]);
+                    hide(xa[0], 0);
+                    hide(xa[1], 1);
+                    float mx = fmaxf(largest(xa[0]), largest(xa[1]));
+                    ptx::tmem_ld_32x32b_x32(s_t + 64, xb[0]);
+                    ptx::tmem_ld_32x32b_x32(s_t + 96, xb[1]);
+                    ptx::tmem_ld_wait(xb[0]);
+                    ptx::tmem_ld_wait(xb[1]);
+                    hide(xb[0], 2);
+                    hide(xb[1], 3);
+                    mx = fmaxf(mx, fmaxf(largest(xb[0]), largest(xb[1])));
                     const bool up = (mx - m) * scale > 8.f || (m == -INFINITY && mx > m);
                     if (__any_sync(0xFFFFFFFFu, up)) {
                         const float m2 = up ? mx : m;
@@ -371,39 +414,48 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                         if (st > lo) {
                             // O so far (complete: its product came before this step's scores)
 #pragma unroll
-                            for (int q = 0; q < D / 32; ++q) {
-                                uint32_t x[32];
-                                ptx::tmem_ld_32x32b_x32(o_t + q * 32, x);
-                                ptx::tmem_ld_wait(x);
+                            for (int q = 0; q < D / 16; ++q) {
+                                uint32_t y[16];
+                                ptx::tmem_ld_32x32b_x16(o_t + q * 16, y);
+                                ptx::tmem_ld_wait16(y);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                                ptx::tmem_st_32x32b_x32(o_t + q * 32, x);
+                                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+                                ptx::tmem_st_32x32b_x16(o_t + q * 16, y);
                             }
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m * scale;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t x[32];
-                        ptx::tmem_ld_32x32b_x32(s_t + q * 32, x);
-                        ptx::tmem_ld_wait(x);
-                        if (masked) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(see[q] >> e & 1)) x[e] = 0xFF800000u;
-                        }
+                    const uint64_t scale2 = pair2(scale, scale), ref2 = pair2(-ref, -ref);
+                    uint64_t sum2[2] = {0, 0};
+                    // P of keys 32 q .. goes where S of later keys was: columns 64 + 16 q ..
+                    auto weigh = [&](const uint32_t (&x)[32], int q) {
                         uint32_t pk[16];
-                        float l0 = 0.f, l1 = 0.f;
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const float u = tl_ex2(fmaf(__uint_as_float(x[e]), scale, -ref));
-                            const float v = tl_ex2(fmaf(__uint_as_float(x[e + 1]), scale, -ref));
-                            l0 += u;
-                            l1 += v;
+                            float u, v;
+                            unpair2(fma2(pair2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, ref2), u, v);
+                            u = tl_ex2(u);
+                            v = tl_ex2(v);
+                            sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pair2(u, v));
                             pk[e / 2] = pack_bf16x2(u, v);
                         }
-                        l += l0 + l1;
-                        ptx::tmem_st_32x32b_x16(s_t + q * 16, pk);
+                        ptx::tmem_st_32x32b_x16(s_t + 64 + q * 16, pk);
+                    };
+                    // keys 0..63 come from TMEM once more, behind the work on the others
+                    ptx::tmem_ld_32x32b_x32(s_t, xa[0]);
+                    weigh(xb[0], 2);
+                    ptx::tmem_ld_32x32b_x32(s_t + 32, xa[1]);
+                    weigh(xb[1], 3);
+                    ptx::tmem_ld_wait(xa[0]);
+                    ptx::tmem_ld_wait(xa[1]);
+                    hide(xa[0], 0);
+                    hide(xa[1], 1);
+                    weigh(xa[0], 0);
+                    weigh(xa[1], 1);
+                    {
+                        float u, v;
+                        unpair2(add2(sum2[0], sum2[1]), u, v);
+                        l += u + v;
                     }
                     ptx::tmem_st_wait();
                     ptx::tc_fence_before();
