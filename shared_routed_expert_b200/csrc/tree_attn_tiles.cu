@@ -13,6 +13,10 @@
 // Roles: warps 0-3 and 4-7 the two halves' softmax, loads of Q and epilogue; warp 8 issues
 // the products; warp 9 streams K and V boxes (one per page piece and 128-byte span) through
 // a ring in shared memory. Every wait is bounded.
+// E4M3 caches: the boxes go to a ring of codes, from which warps 10 and 11 write K and V as
+// fp16 (exact) to the products' ring. Q rows are scaled by a power of two to fp16 (exact for
+// everything within 2^-28 of the row's largest entry) and P is fp16. (E4M3 operands would
+// need P in 4 significant bits.)
 #include "kernels.cuh"
 #include "tc_ptx.cuh"
 #include "tree_attn.cuh"
@@ -22,18 +26,23 @@ namespace sre {
 namespace {
 
 constexpr int TK = 128;                  // keys per step
-constexpr int TL_THREADS = 320;
+constexpr int TL_THREADS = 320, TL_THREADS_F8 = 384;
 constexpr int kTileExtra = 2;            // what an item costs besides its steps, in steps
 constexpr int kInfo = 8;                 // steps whose key masks are kept (the producer is at most 6 ahead)
 
-template <int D>
+template <int D, bool F8>
 struct Tile {
     static constexpr int SPANS = D * 2 / 128;
     static constexpr int SPAN = 128 * 128;                         // bytes of a span of 128 rows
     static constexpr int QHALF = SPANS * SPAN;
-    static constexpr int SLOT = SPANS * SPAN;                      // K or V of a step
-    static constexpr int NS = D == 128 ? 5 : 10;
-    static constexpr int SMEM = 2 * QHALF + NS * SLOT + 1024;
+    static constexpr int SLOT = SPANS * SPAN;                      // K or V of a step, 16 bits each
+    static constexpr int NS = F8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
+    static constexpr int CODES = TK * D;                           // K or V of a step as E4M3 codes
+    static constexpr int NR = F8 ? 4 : 0;
+    static constexpr int SMEM = 2 * QHALF + NS * SLOT + NR * CODES + 1024;
+    // what is loaded by TMA, at the rows' own width
+    static constexpr int ROWB = F8 ? D : 128;
+    static constexpr int LOAD_SPANS = F8 ? 1 : SPANS, LOAD_SPAN = TK * ROWB;
 };
 
 struct TileParams {
@@ -62,6 +71,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// two E4M3 codes (the low 16 bits) -> two fp16
+__device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t v) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
+    return r;
+}
+
 __device__ __forceinline__ float tl_ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -69,7 +85,7 @@ __device__ __forceinline__ float tl_ex2(float x) {
 }
 
 // A row of an item again, key by key (a rare path, kept out of the main code's registers)
-template <int D>
+template <int D, bool F8>
 __device__ __noinline__ void redo_row(const AttnArgs& a, const Cursor& c, int i, int head, int lo, int hi, float* o, float* ml,
                                       int lane) {
     constexpr int EPL = D / 32;
@@ -79,7 +95,7 @@ __device__ __noinline__ void redo_row(const AttnArgs& a, const Cursor& c, int i,
         q[j] = bf16_to_f32(a.q[(c.s.row0 + i) * a.q_stride + head * D + lane * EPL + j]);
         acc[j] = 0.f;
     }
-    attend_row<EPL, false>(a, c.b, c.s, i, c.h, q, lo, hi, m, l, acc, lane);
+    attend_row<EPL, F8>(a, c.b, c.s, i, c.h, q, lo, hi, m, l, acc, lane);
     if (o != nullptr) {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) o[lane * EPL + j] = acc[j];
@@ -97,27 +113,34 @@ __device__ __noinline__ void redo_row(const AttnArgs& a, const Cursor& c, int i,
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_constant__ TileParams p) {
-    using S = Tile<D>;
-    constexpr int NS = S::NS;
+template <int D, bool F8>
+__global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kernel(const __grid_constant__ TileParams p) {
+    using S = Tile<D, F8>;
+    constexpr int NS = S::NS, NR = S::NR > 0 ? S::NR : 1;
     constexpr Tiling G{kTileRows, TK, kTileExtra};
     extern __shared__ __align__(1024) unsigned char tl_raw[];
     __shared__ ScanShared scan;
     __shared__ uint64_t full[NS], empty[NS], q_ready[2], s_full[2], p_ready[2], o_full[2], tail_bar, drain_bar;
+    __shared__ uint64_t raw_full[NR], raw_free[NR];
+    __shared__ float q_scale[2][128];    // E4M3: what a row of Q was divided by, times the scale
     __shared__ uint32_t info[kInfo][4];  // keys of a step that were loaded
     __shared__ uint32_t tmem_base_s;
     __shared__ int s_abort;
     unsigned char* smem = tl_raw + ((1024 - (ptx::smem_u32(tl_raw) & 1023)) & 1023);
     unsigned char* ring = smem + 2 * S::QHALF;
+    unsigned char* codes = ring + NS * S::SLOT;
     volatile int* abort_flag = &s_abort;
     const AttnArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         s_abort = 0;
         for (int i = 0; i < NS; ++i) {
-            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&full[i], F8 ? 2 : 1);
             ptx::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < NR; ++i) {
+            ptx::mbar_init(&raw_full[i], 1);
+            ptx::mbar_init(&raw_free[i], 2);
         }
         for (int h = 0; h < 2; ++h) {
             ptx::mbar_init(&q_ready[h], 128);
@@ -194,23 +217,23 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                 if (lane < 4) info[step_no % kInfo][lane] = word;
                 __syncwarp();
                 const bool partial = __any_sync(0xFFFFFFFFu, lane < 4 && word != 0xFFFFFFFFu);
-                const uint32_t bytes = static_cast<uint32_t>(__popc(goods)) * box * 128u * S::SPANS;
+                const uint32_t bytes = static_cast<uint32_t>(__popc(goods)) * box * S::ROWB * S::LOAD_SPANS;
                 const int slot_in_page = c & ((1 << a.c.page_shift) - 1);
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const uint32_t sl = n % NS;
-                    ok = ok && ptx::mbar_wait(&empty[sl], ((n / NS) & 1u) ^ 1u, abort_flag, p.wait_limit, a.status, 1u);
+                    const uint32_t sl = F8 ? n % NR : n % NS, use = F8 ? n / NR : n / NS;
+                    ok = ok && ptx::mbar_wait(F8 ? &raw_free[sl] : &empty[sl], (use & 1u) ^ 1u, abort_flag, p.wait_limit, a.status, 1u);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
-                    const bool tail = kv == 1 && partial;
-                    uint64_t* bar = tail ? &tail_bar : &full[sl];
+                    const bool tail = !F8 && kv == 1 && partial;
+                    uint64_t* bar = F8 ? &raw_full[sl] : (tail ? &tail_bar : &full[sl]);
                     if (lane == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
                     __syncwarp();
-                    unsigned char* dst = ring + sl * S::SLOT;
+                    unsigned char* dst = F8 ? codes + sl * S::CODES : ring + sl * S::SLOT;
                     if (good) {
 #pragma unroll
-                        for (int sp = 0; sp < S::SPANS; ++sp)
-                            ptx::tma_load_5d(dst + sp * S::SPAN + lane * box * 128, kv ? &p.tv : &p.tk, bar, 0, slot_in_page,
+                        for (int sp = 0; sp < S::LOAD_SPANS; ++sp)
+                            ptx::tma_load_5d(dst + sp * S::LOAD_SPAN + lane * box * S::ROWB, kv ? &p.tv : &p.tk, bar, 0, slot_in_page,
                                              sp, cur.h, page);
                     }
                     if (tail) {
@@ -236,19 +259,20 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
         }
         if (lane == 0 && *abort_flag) {
             // every copy in flight lands before the block's memory goes away
-            for (uint32_t i = 0; i < NS; ++i) {
-                const uint32_t uses = n > i ? (n - i + NS - 1) / NS : 0;   // times slot i was armed
+            constexpr uint32_t kSlots = F8 ? NR : NS;
+            for (uint32_t i = 0; i < kSlots; ++i) {
+                const uint32_t uses = n > i ? (n - i + kSlots - 1) / kSlots : 0;   // times slot i was armed
                 if (uses == 0) continue;
                 const long long t0 = clock64();
-                while (!ptx::mbar_try_wait(&full[i], (uses - 1) & 1u) && clock64() - t0 < p.wait_limit) {
+                while (!ptx::mbar_try_wait(F8 ? &raw_full[i] : &full[i], (uses - 1) & 1u) && clock64() - t0 < p.wait_limit) {
                 }
             }
         }
     } else if (warp == 8) {
         // ------------------------------------------------------------ products
         if (lane == 0) {
-            constexpr uint32_t IS = ptx::instr_desc(128, TK, 1);
-            constexpr uint32_t IO = ptx::instr_desc(128, D, 1) | ptx::kBMnMajor;
+            constexpr uint32_t IS = ptx::instr_desc(128, TK, F8 ? 0 : 1);
+            constexpr uint32_t IO = ptx::instr_desc(128, D, F8 ? 0 : 1) | ptx::kBMnMajor;
             const uint32_t q_u = ptx::smem_u32(smem), ring_u = ptx::smem_u32(ring);
             uint32_t n = 0, qp[2] = {0, 0}, pp[2] = {0, 0};
             bool ok = true;
@@ -319,12 +343,54 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
             while (!ptx::mbar_try_wait(&drain_bar, 0) && clock64() - t0 < p.wait_limit) {
             }
         }
+    } else if (F8 && warp >= 10) {
+        // ------------------------------------------------------------ E4M3 codes to fp16
+        constexpr int CPR = D / 16;                                // 16-byte chunks of codes per key
+        const int tid = threadIdx.x - 320;
+        uint32_t n = 0, step_no = 0;
+        bool ok = true;
+        while (ok && cur.segment(a, G, left, lo, hi)) {
+            for (int st = lo; st < hi && ok; ++st, ++step_no) {
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const uint32_t sl = n % NS, rw = n % NR;
+                    ok = ptx::mbar_wait(&raw_full[rw], (n / NR) & 1u, abort_flag, p.wait_limit, a.status, 10u) &&
+                         ptx::mbar_wait(&empty[sl], ((n / NS) & 1u) ^ 1u, abort_flag, p.wait_limit, a.status, 11u);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    const unsigned char* src = codes + rw * S::CODES;
+                    unsigned char* dst = ring + sl * S::SLOT;
+#pragma unroll 4
+                    for (int c = tid; c < TK * CPR; c += 64) {
+                        const int key = c / CPR, ch = c % CPR;
+                        const int swz = S::ROWB == 128 ? key & 7 : (key >> 1) & 3;
+                        uint4 v = *reinterpret_cast<const uint4*>(src + key * S::ROWB + ((ch ^ swz) << 4));
+                        // keys that are not there count as zero, not as whatever lies there
+                        if (!(info[step_no % kInfo][key >> 5] >> (key & 31) & 1)) v = make_uint4(0, 0, 0, 0);
+                        const uint4 lo16 = make_uint4(f16_of_e4m3(v.x), f16_of_e4m3(v.x >> 16), f16_of_e4m3(v.y), f16_of_e4m3(v.y >> 16));
+                        const uint4 hi16 = make_uint4(f16_of_e4m3(v.z), f16_of_e4m3(v.z >> 16), f16_of_e4m3(v.w), f16_of_e4m3(v.w >> 16));
+                        // dimensions 16 ch .. of the key: two chunks of span ch / 4; the spans' lanes take them
+                        // in opposite order, for the banks
+                        unsigned char* at = dst + (ch >> 2) * S::SPAN + key * 128;
+                        const int first = 2 * (ch & 3) + ((ch >> 2) & 1), second = first ^ 1;
+                        *reinterpret_cast<uint4*>(at + ((first ^ (key & 7)) << 4)) = (first & 1) ? hi16 : lo16;
+                        *reinterpret_cast<uint4*>(at + ((second ^ (key & 7)) << 4)) = (second & 1) ? hi16 : lo16;
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::mbar_arrive(&full[sl]);
+                        ptx::mbar_arrive(&raw_free[rw]);
+                    }
+                }
+            }
+        }
     } else {
         // ------------------------------------------------------------ softmax of one half
         const int h = warp >> 2, sub = warp & 3;
         const uint32_t s_t = tmem + h * 128 + (static_cast<uint32_t>(sub * 32) << 16);
         const uint32_t o_t = s_t - h * 128 + 256 + h * 128;
-        const float scale = fmaxf(fabsf(a.scale_log2), 1.0e-37f);  // (0 would turn what is not seen into NaN)
+        const float all_scale = fmaxf(fabsf(a.scale_log2), 1.0e-37f);   // (0 would turn what is not seen into NaN)
         const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;   // a negative scale: q changes sign instead
         uint32_t sp = 0, op = 0, step_no = 0;
         bool ok = true;
@@ -348,11 +414,33 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                                                                 static_cast<long long>(cur.h * a.group + rr - i * a.group) * D + ch * 8);
                             v.x ^= sign; v.y ^= sign; v.z ^= sign; v.w ^= sign;
                         }
+                        if constexpr (F8) {
+                            // the row's largest finite entry, over the D / 8 lanes that hold it
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            float mx = 0.f;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float x = fabsf(__uint_as_float(w[j] << 16)), y = fabsf(__uint_as_float(w[j] & 0xFFFF0000u));
+                                mx = x < INFINITY ? fmaxf(mx, x) : mx;
+                                mx = y < INFINITY ? fmaxf(mx, y) : mx;
+                            }
+#pragma unroll
+                            for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                            const int ex = f16_chunk_exp(mx);
+                            const float d = exp2_int(-ex);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                w[j] = pack_f16x2(__uint_as_float(w[j] << 16) * d, __uint_as_float(w[j] & 0xFFFF0000u) * d);
+                            v = make_uint4(w[0], w[1], w[2], w[3]);
+                            if (ch == 0) q_scale[h][r] = all_scale * exp2_int(ex);
+                        }
                         *reinterpret_cast<uint4*>(dst + (ch >> 3) * S::SPAN + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
                     }
                     ptx::fence_proxy_async_smem();
                     ptx::mbar_arrive(&q_ready[h]);
                 }
+                __syncwarp();
+                const float scale = F8 ? fmaxf(q_scale[h][sub * 32 + lane], 1.0e-37f) : all_scale;
                 const int keys = tile_keys(a, s, cur.mt, G.M);
                 const int rr = r_first + min(sub * 32 + lane, rows - 1);   // this thread's row (or the last one)
                 const int i = token_of(a, rr);
@@ -437,7 +525,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                             u = tl_ex2(u);
                             v = tl_ex2(v);
                             sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pair2(u, v));
-                            pk[e / 2] = pack_bf16x2(u, v);
+                            pk[e / 2] = F8 ? pack_f16x2(u, v) : pack_bf16x2(u, v);
                         }
                         ptx::tmem_st_32x32b_x16(s_t + 64 + q * 16, pk);
                     };
@@ -523,7 +611,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
                     again &= again - 1;
                     const int ri = __shfl_sync(0xFFFFFFFFu, i, src), rh = __shfl_sync(0xFFFFFFFFu, head, src);
                     const size_t sr = slot_row - lane + src;
-                    redo_row<D>(a, cur, ri, rh, lo * TK, min(hi * TK, keys), whole ? nullptr : p.part.o + sr * D,
+                    redo_row<D, F8>(a, cur, ri, rh, lo * TK, min(hi * TK, keys), whole ? nullptr : p.part.o + sr * D,
                                 p.part.ml + sr * 2, lane);
                 }
             } else {
@@ -540,9 +628,9 @@ __global__ void __launch_bounds__(TL_THREADS, 1) tiles_kernel(const __grid_const
     }
 }
 
-template <int D>
+template <int D, bool F8>
 cudaError_t launch_tiles(const AttnArgs& a, void* partials, int sms, cudaStream_t st) {
-    using S = Tile<D>;
+    using S = Tile<D, F8>;
     TileParams p;
     p.a = a;
     const int page = 1 << a.c.page_shift;
@@ -552,11 +640,11 @@ cudaError_t launch_tiles(const AttnArgs& a, void* partials, int sms, cudaStream_
     if (!make_kv_map(&p.tk, a, false, box) || !make_kv_map(&p.tv, a, true, box)) return cudaErrorInvalidValue;
     const int blocks = sms < kTileBlocks ? sms : kTileBlocks;
     p.part = partials_at(partials, blocks, kTileRows);
-    const cudaError_t e = cudaFuncSetAttribute(tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(tiles_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
     {
         ProfileScope ps("tree_attention", st);
-        tiles_kernel<D><<<blocks, TL_THREADS, S::SMEM, st>>>(p);
+        tiles_kernel<D, F8><<<blocks, F8 ? TL_THREADS_F8 : TL_THREADS, S::SMEM, st>>>(p);
         note_launch();
     }
     const cudaError_t le = cudaGetLastError();
@@ -567,7 +655,7 @@ cudaError_t launch_tiles(const AttnArgs& a, void* partials, int sms, cudaStream_
 }  // namespace
 
 bool tree_attn_tiles_apply(const AttnArgs& a) {
-    return !a.f8 && a.head_dim <= 128 && static_cast<long long>(a.c.max_new) * a.group > kSmallRows;
+    return a.head_dim <= 128 && static_cast<long long>(a.c.max_new) * a.group > kSmallRows;
 }
 
 cudaError_t launch_tree_attn_tiles(const AttnArgs& a, void* partials, cudaStream_t st) {
@@ -575,7 +663,8 @@ cudaError_t launch_tree_attn_tiles(const AttnArgs& a, void* partials, cudaStream
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (sms <= 0) sms = 148;
-    return a.head_dim == 64 ? launch_tiles<64>(a, partials, sms, st) : launch_tiles<128>(a, partials, sms, st);
+    if (a.head_dim == 64) return a.f8 ? launch_tiles<64, true>(a, partials, sms, st) : launch_tiles<64, false>(a, partials, sms, st);
+    return a.f8 ? launch_tiles<128, true>(a, partials, sms, st) : launch_tiles<128, false>(a, partials, sms, st);
 }
 
 }  // namespace sre
