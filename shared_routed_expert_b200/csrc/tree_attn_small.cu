@@ -259,19 +259,24 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
 
         // ---- Q to shared memory: D / 8 lanes per row, 16 bytes each; rows behind the last are 0
         {
-            constexpr int LPR = D / 8, RPI = NW * 32 / LPR;
+            constexpr int LPR = D / 8, RPI = NW * 32 / LPR, BATCH = (M + RPI - 1) / RPI;
             const uint32_t sign = flip ? 0x80008000u : 0u;
             const int ch = threadIdx.x % LPR;
+            uint4 in[BATCH];                                       // all loads in flight before the stores
 #pragma unroll
-            for (int r = threadIdx.x / LPR; r < (M + RPI - 1) / RPI * RPI; r += RPI) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                const int rr = cur.mt * M + r;
+            for (int k = 0; k < BATCH; ++k) {
+                const int r = threadIdx.x / LPR + k * RPI, rr = cur.mt * M + r;
+                in[k] = make_uint4(0, 0, 0, 0);
                 if (r < M && rr < rows) {
                     const int i = token_of(a, rr);
-                    v = *reinterpret_cast<const uint4*>(a.q + (s.row0 + i) * a.q_stride +
-                                                        static_cast<long long>(cur.h * a.group + rr - i * a.group) * D + ch * 8);
-                    v.x ^= sign; v.y ^= sign; v.z ^= sign; v.w ^= sign;
+                    in[k] = __ldg(reinterpret_cast<const uint4*>(
+                        a.q + (s.row0 + i) * a.q_stride + static_cast<long long>(cur.h * a.group + rr - i * a.group) * D + ch * 8));
                 }
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int r = threadIdx.x / LPR + k * RPI;
+                const uint4 v = make_uint4(in[k].x ^ sign, in[k].y ^ sign, in[k].z ^ sign, in[k].w ^ sign);
                 if constexpr (!F8) {
                     if (r < M) *reinterpret_cast<uint4*>(q_smem + r * S::QPITCH + ch * 16) = v;
                 } else {
@@ -699,8 +704,10 @@ cudaError_t launch_d(const AttnArgs& a, void* partials, int sms, cudaStream_t st
     // rows of a tile: the smallest that holds a sequence's rows
     const long long rows = static_cast<long long>(a.c.max_new) * a.group;
     if (rows <= 16) return launch_cfg<D, F8, 1>(a, partials, sms, st);
-    if (rows <= 32) return launch_cfg<D, F8, 2>(a, partials, sms, st);
-    return launch_cfg<D, F8, 4>(a, partials, sms, st);
+    if constexpr (D == 256) {                                      // (narrower heads take tree_attn_tiles.cu then)
+        if (rows > 32) return launch_cfg<D, F8, 4>(a, partials, sms, st);
+    }
+    return launch_cfg<D, F8, 2>(a, partials, sms, st);
 }
 
 }  // namespace

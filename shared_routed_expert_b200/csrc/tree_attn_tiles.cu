@@ -10,6 +10,8 @@
 // While one half's exponentials run, the other half's products do. The running maximum is
 // raised (and O rescaled, in TMEM) only when a row's grows by more than 2^8, so that
 // rescaling is rare; sums and statistics are fp32, P is rounded to bf16 for the product.
+// A tile of no more than 128 rows (short drafts, the ends of sequences) has both halves work
+// on the same rows, on every second step each, and the first half join the two sums.
 // Roles: warps 0-3 and 4-7 the two halves' softmax, loads of Q and epilogue; warp 8 issues
 // the products; warp 9 streams K and V boxes (one per page piece and 128-byte span) through
 // a ring in shared memory. Every wait is bounded.
@@ -28,6 +30,10 @@ namespace {
 constexpr int TK = 128;                  // keys per step
 constexpr int TL_THREADS = 320, TL_THREADS_F8 = 384;
 constexpr int kTileExtra = 2;            // what an item costs besides its steps, in steps
+// Rows of a kv head from which this kernel takes over. Above 32 rows each 16 of them cost the
+// other kernel (tree_attn_small.cu) a pass over K and V in shared memory: 32 sequences of 4 rows
+// of 96 heads (48 rows a kv head), 566 MB of bf16 cache: 138 us here, 195 us there.
+constexpr int kTileLeastRows = 32;
 constexpr int kInfo = 8;                 // steps whose key masks are kept (the producer is at most 6 ahead)
 
 template <int D, bool F8>
@@ -120,7 +126,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
     constexpr Tiling G{kTileRows, TK, kTileExtra};
     extern __shared__ __align__(1024) unsigned char tl_raw[];
     __shared__ ScanShared scan;
-    __shared__ uint64_t full[NS], empty[NS], q_ready[2], s_full[2], p_ready[2], o_full[2], tail_bar, drain_bar;
+    __shared__ uint64_t full[NS], empty[NS], q_ready[2], s_full[2], p_ready[2], o_full[2], x_ready, x_done, tail_bar, drain_bar;
     __shared__ uint64_t raw_full[NR], raw_free[NR];
     __shared__ float q_scale[2][128];    // E4M3: what a row of Q was divided by, times the scale
     __shared__ uint32_t info[kInfo][4];  // keys of a step that were loaded
@@ -129,6 +135,8 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
     unsigned char* smem = tl_raw + ((1024 - (ptx::smem_u32(tl_raw) & 1023)) & 1023);
     unsigned char* ring = smem + 2 * S::QHALF;
     unsigned char* codes = ring + NS * S::SLOT;
+    // where both halves work on the same rows, the second half's maxima (base 2) and sums lie in its Q
+    float2* x_ml = reinterpret_cast<float2*>(smem + S::QHALF);
     volatile int* abort_flag = &s_abort;
     const AttnArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -148,6 +156,8 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
             ptx::mbar_init(&p_ready[h], 128);
             ptx::mbar_init(&o_full[h], 1);
         }
+        ptx::mbar_init(&x_ready, 128);
+        ptx::mbar_init(&x_done, 128);
         ptx::mbar_init(&tail_bar, 1);
         ptx::mbar_init(&drain_bar, 1);
         ptx::fence_mbar_init();
@@ -285,8 +295,8 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
             const uint32_t k_hi = static_cast<uint32_t>(d_k >> 32), k_lo = static_cast<uint32_t>(d_k);
             const uint32_t mn_hi = static_cast<uint32_t>(d_mn >> 32), mn_lo = static_cast<uint32_t>(d_mn);
             auto desc = [](uint32_t hi_w, uint32_t lo_w) { return static_cast<uint64_t>(hi_w) << 32 | lo_w; };
-            auto scores = [&](int h, uint32_t kslot) {
-                const uint32_t ka = k_lo + ((ring_u + kslot * S::SLOT) >> 4), qa = k_lo + ((q_u + h * S::QHALF) >> 4);
+            auto scores = [&](int h, int qh, uint32_t kslot) {
+                const uint32_t ka = k_lo + ((ring_u + kslot * S::SLOT) >> 4), qa = k_lo + ((q_u + qh * S::QHALF) >> 4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = ((k >> 2) * S::SPAN + (k & 3) * 32) >> 4;
@@ -301,13 +311,40 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
             };
             while (ok && cur.segment(a, G, left, lo, hi)) {
                 const bool two = cur.s.n * a.group - cur.mt * G.M > 128;
+                if (!two && hi - lo > 1) {
+                    // half h takes steps lo + h, lo + h + 2, ... of the same rows
+                    if (!wait(&q_ready[0], qp[0], 4u)) break;
+                    qp[0] ^= 1u;
+#pragma unroll 1
+                    for (int st = lo - 2; st < hi; ++st) {
+                        const int h = (st - lo) & 1;
+                        const uint32_t kn = n + 2 * (st + 2 - lo), vn = n + 2 * (st - lo) + 1;
+                        if (st >= lo) {
+                            if (!wait(&full[vn % NS], (vn / NS) & 1u, 3u) || !wait(&p_ready[h], pp[h], 5u)) break;
+                            pp[h] ^= 1u;
+                            ptx::tc_fence_after();
+                            values(h, vn % NS, st > lo + 1);
+                            ptx::mma_commit(&empty[vn % NS]);
+                            if (st + 2 >= hi) ptx::mma_commit(&o_full[h]);
+                        }
+                        if (st + 2 < hi) {
+                            if (!wait(&full[kn % NS], (kn / NS) & 1u, 3u)) break;
+                            ptx::tc_fence_after();
+                            scores(h, 0, kn % NS);
+                            ptx::mma_commit(&s_full[h]);
+                            ptx::mma_commit(&empty[kn % NS]);
+                        }
+                    }
+                    n += 2 * (hi - lo);
+                    continue;
+                }
                 if (!wait(&full[n % NS], (n / NS) & 1u, 3u)) break;
 #pragma unroll 1
                 for (int h = 0; h < (two ? 2 : 1); ++h) {
                     if (!wait(&q_ready[h], qp[h], 4u)) break;
                     qp[h] ^= 1u;
                     ptx::tc_fence_after();
-                    scores(h, n % NS);
+                    scores(h, h, n % NS);
                     ptx::mma_commit(&s_full[h]);
                 }
                 if (!ok) break;
@@ -327,7 +364,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                         if (more) {
                             if (h == 0 && !wait(&full[kn % NS], (kn / NS) & 1u, 3u)) break;
                             ptx::tc_fence_after();
-                            scores(h, kn % NS);
+                            scores(h, h, kn % NS);
                             ptx::mma_commit(&s_full[h]);
                             if (last) ptx::mma_commit(&empty[kn % NS]);
                         } else {
@@ -392,52 +429,64 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
         const uint32_t o_t = s_t - h * 128 + 256 + h * 128;
         const float all_scale = fmaxf(fabsf(a.scale_log2), 1.0e-37f);   // (0 would turn what is not seen into NaN)
         const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;   // a negative scale: q changes sign instead
-        uint32_t sp = 0, op = 0, step_no = 0;
+        uint32_t sp = 0, op = 0, xp = 0, step_no = 0;
         bool ok = true;
         while (ok && cur.segment(a, G, left, lo, hi)) {
             const SeqInfo s = cur.s;
-            const int rows = s.n * a.group - cur.mt * G.M - h * 128;   // of this half
+            const int in_tile = s.n * a.group - cur.mt * G.M;
+            const bool share = in_tile <= 128 && hi - lo > 1;          // both halves on the same rows
+            const int rows = share ? in_tile : in_tile - h * 128;      // of this half
             if (rows > 0) {
-                const int r_first = cur.mt * G.M + h * 128;
+                const int r_first = cur.mt * G.M + (share ? 0 : h * 128);
                 // ---- Q to shared memory: a row per D / 8 lanes, 16 bytes each
-                {
+                // (both halves write the same rows' scales, each its own copy)
+                if (!share || h == 0 || F8) {
                     constexpr int LPR = D / 8, RPI = 32 / LPR;
                     unsigned char* dst = smem + h * S::QHALF;
                     const int ch = lane % LPR;                     // 16-byte chunk of the row
-#pragma unroll 8
-                    for (int k = 0; k < 32 / RPI; ++k) {
-                        const int r = sub * 32 + k * RPI + lane / LPR;
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (r < rows) {
-                            const int rr = r_first + r, i = token_of(a, rr);
-                            v = *reinterpret_cast<const uint4*>(a.q + (s.row0 + i) * a.q_stride +
-                                                                static_cast<long long>(cur.h * a.group + rr - i * a.group) * D + ch * 8);
-                            v.x ^= sign; v.y ^= sign; v.z ^= sign; v.w ^= sign;
-                        }
-                        if constexpr (F8) {
-                            // the row's largest finite entry, over the D / 8 lanes that hold it
-                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                            float mx = 0.f;
+                    constexpr int BATCH = 8;                       // loads in flight together, before the stores
+#pragma unroll 1
+                    for (int k0 = 0; k0 < 32 / RPI; k0 += BATCH) {
+                        uint4 in[BATCH];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float x = fabsf(__uint_as_float(w[j] << 16)), y = fabsf(__uint_as_float(w[j] & 0xFFFF0000u));
-                                mx = x < INFINITY ? fmaxf(mx, x) : mx;
-                                mx = y < INFINITY ? fmaxf(mx, y) : mx;
+                        for (int k = 0; k < BATCH; ++k) {
+                            const int r = sub * 32 + (k0 + k) * RPI + lane / LPR;
+                            in[k] = make_uint4(0, 0, 0, 0);
+                            if (r < rows) {
+                                const int rr = r_first + r, i = token_of(a, rr);
+                                in[k] = __ldg(reinterpret_cast<const uint4*>(
+                                    a.q + (s.row0 + i) * a.q_stride + static_cast<long long>(cur.h * a.group + rr - i * a.group) * D + ch * 8));
                             }
-#pragma unroll
-                            for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-                            const int ex = f16_chunk_exp(mx);
-                            const float d = exp2_int(-ex);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                w[j] = pack_f16x2(__uint_as_float(w[j] << 16) * d, __uint_as_float(w[j] & 0xFFFF0000u) * d);
-                            v = make_uint4(w[0], w[1], w[2], w[3]);
-                            if (ch == 0) q_scale[h][r] = all_scale * exp2_int(ex);
                         }
-                        *reinterpret_cast<uint4*>(dst + (ch >> 3) * S::SPAN + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+#pragma unroll
+                        for (int k = 0; k < BATCH; ++k) {
+                            const int r = sub * 32 + (k0 + k) * RPI + lane / LPR;
+                            uint4 v = make_uint4(in[k].x ^ sign, in[k].y ^ sign, in[k].z ^ sign, in[k].w ^ sign);
+                            if constexpr (F8) {
+                                // the row's largest finite entry, over the D / 8 lanes that hold it
+                                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                                float mx = 0.f;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const float x = fabsf(__uint_as_float(w[j] << 16)), y = fabsf(__uint_as_float(w[j] & 0xFFFF0000u));
+                                    mx = x < INFINITY ? fmaxf(mx, x) : mx;
+                                    mx = y < INFINITY ? fmaxf(mx, y) : mx;
+                                }
+#pragma unroll
+                                for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                                const int ex = f16_chunk_exp(mx);
+                                const float d = exp2_int(-ex);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    w[j] = pack_f16x2(__uint_as_float(w[j] << 16) * d, __uint_as_float(w[j] & 0xFFFF0000u) * d);
+                                v = make_uint4(w[0], w[1], w[2], w[3]);
+                                if (ch == 0) q_scale[h][r] = all_scale * exp2_int(ex);
+                            }
+                            *reinterpret_cast<uint4*>(dst + (ch >> 3) * S::SPAN + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+                        }
                     }
                     ptx::fence_proxy_async_smem();
-                    ptx::mbar_arrive(&q_ready[h]);
+                    if (!share || h == 0) ptx::mbar_arrive(&q_ready[h]);
                 }
                 __syncwarp();
                 const float scale = F8 ? fmaxf(q_scale[h][sub * 32 + lane], 1.0e-37f) : all_scale;
@@ -447,14 +496,15 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                 // steps that end in front of this key need no look at what a row sees
                 const int clear = a.mask != nullptr ? s.ctx : s.ctx + token_of(a, r_first) + 1;
                 float m = -INFINITY, l = 0.f;
-                for (int st = lo; st < hi; ++st, ++step_no) {
+                const int by = share ? 2 : 1, from = share ? lo + h : lo;
+                for (int st = from; st < hi; st += by) {
                     ok = ptx::mbar_wait(&s_full[h], sp, abort_flag, p.wait_limit, a.status, 6u);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     sp ^= 1u;
                     ptx::tc_fence_after();
                     const int c0 = st * TK;
-                    const uint32_t* word = info[step_no % kInfo];
+                    const uint32_t* word = info[(step_no + st - lo) % kInfo];
                     const bool masked = c0 + TK > clear || (word[0] & word[1] & word[2] & word[3]) != 0xFFFFFFFFu;
                     uint32_t see[4];
                     if (masked) {
@@ -499,7 +549,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                         const float f = up ? tl_ex2((m - m2) * scale) : 1.f;
                         m = m2;
                         l *= f;
-                        if (st > lo) {
+                        if (st > from) {
                             // O so far (complete: its product came before this step's scores)
 #pragma unroll
                             for (int q = 0; q < D / 16; ++q) {
@@ -549,6 +599,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                     ptx::tc_fence_before();
                     ptx::mbar_arrive(&p_ready[h]);
                 }
+                step_no += hi - lo;
                 if (!ok) break;
                 // ---- epilogue: a thread's row of O
                 ok = ptx::mbar_wait(&o_full[h], op, abort_flag, p.wait_limit, a.status, 8u);
@@ -556,11 +607,36 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                 if (!ok) break;
                 op ^= 1u;
                 ptx::tc_fence_after();
+                float m2 = l == 0.f ? -INFINITY : m * scale, f0 = 1.f, f1 = 0.f;
+                if (share) {
+                    const int x = sub * 32 + lane;
+                    if (h == 1) {
+                        // the first half reads this half's O; the next one is not begun before it has
+                        x_ml[x] = make_float2(m2, l);
+                        ptx::tc_fence_before();
+                        ptx::mbar_arrive(&x_ready);
+                        ok = ptx::mbar_wait(&x_done, xp, abort_flag, p.wait_limit, a.status, 12u);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        xp ^= 1u;
+                        continue;
+                    }
+                    ok = ptx::mbar_wait(&x_ready, xp, abort_flag, p.wait_limit, a.status, 13u);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    xp ^= 1u;
+                    ptx::tc_fence_after();
+                    const float2 o = x_ml[x];
+                    const float both = fmaxf(m2, o.x), base = both == -INFINITY ? 0.f : both;
+                    f0 = tl_ex2(m2 - base);
+                    f1 = tl_ex2(o.x - base);
+                    m2 = both;
+                    l = l * f0 + o.y * f1;
+                }
                 const bool mine = sub * 32 + lane < rows;
                 const int head = cur.h * a.group + rr - i * a.group;
                 const long long row = s.row0 + i;
                 const bool whole = lo == 0 && hi == cur.steps;
-                const size_t slot_row = (2 * static_cast<size_t>(blockIdx.x) + (lo == 0)) * kTileRows + h * 128 + sub * 32 + lane;
+                const size_t slot_row = (2 * static_cast<size_t>(blockIdx.x) + (lo == 0)) * kTileRows + h * 128 + sub * 32 + lane;   // (share: h is 0)
                 if (threadIdx.x == 0 && lo == 0 && !whole)         // (the last of the share; half 0 always has rows)
                     p.part.items[blockIdx.x] =
                         JoinItem{item_shares(shares, cur, G, x1, left).y, s.row0, s.n * a.group, cur.h, cur.mt};
@@ -573,6 +649,14 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                     uint32_t x[32];
                     ptx::tmem_ld_32x32b_x32(o_t + q * 32, x);
                     ptx::tmem_ld_wait(x);
+                    if (share) {
+                        uint32_t y[32];
+                        ptx::tmem_ld_32x32b_x32(o_t + 128 + q * 32, y);
+                        ptx::tmem_ld_wait(y);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            x[e] = __float_as_uint(__uint_as_float(x[e]) * f0 + __uint_as_float(y[e]) * f1);
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) nan |= __uint_as_float(x[e]) != __uint_as_float(x[e]);
                     if (mine && whole) {
@@ -594,10 +678,10 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                     __syncwarp();
                 }
                 ptx::tc_fence_before();
-                const float m2 = m * scale;
+                if (share) ptx::mbar_arrive(&x_done);
                 if (mine) {
                     if (!whole) {
-                        part_ml[0] = l == 0.f ? -INFINITY : m2;
+                        part_ml[0] = m2;
                         part_ml[1] = l;
                     } else if (a.lse != nullptr) {
                         a.lse[row * a.n_q + head] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * kLn2F;
@@ -655,7 +739,7 @@ cudaError_t launch_tiles(const AttnArgs& a, void* partials, int sms, cudaStream_
 }  // namespace
 
 bool tree_attn_tiles_apply(const AttnArgs& a) {
-    return a.head_dim <= 128 && static_cast<long long>(a.c.max_new) * a.group > kSmallRows;
+    return a.head_dim <= 128 && static_cast<long long>(a.c.max_new) * a.group > kTileLeastRows;
 }
 
 cudaError_t launch_tree_attn_tiles(const AttnArgs& a, void* partials, cudaStream_t st) {
