@@ -5,9 +5,13 @@
 //   u = v / sqrt(mean(v^2) + eps) * w, the first rot_dim dimensions of u rotated
 //   by the table row positions[t] (q and k heads, as in qknorm.cu);
 //   q heads -> q_out, k heads -> K cache, v heads unchanged -> V cache.
-// Bound by HBM: each head is read and written once. One warp takes HPW
-// consecutive heads of a token, lane l holding dimensions EPL*l .. EPL*l + EPL-1,
-// all its loads issued before the arithmetic.
+// Each head is read and written once; what the kernel spends beside that is instructions, so
+// lanes hold 8 dimensions each (16-byte loads and stores) and a warp's instruction covers 1, 2
+// or 4 heads of 256, 128 or 64 dimensions. The sums of squares are added in the order of
+// qknorm.cu's 32 lanes (partial sums of head_dim / 32 dimensions, a butterfly over them), and
+// the products are formed alike, so q rows and bf16 keys have the same bits. (4 dimensions a
+// lane and a head per instruction: 104 instructions a head, 86 us for 5 prompts of 5949 tokens,
+// 96 + 8 + 8 heads of 128.)
 #include "kernels.cuh"
 #include "kv_cache.cuh"
 
@@ -17,41 +21,34 @@ namespace {
 
 constexpr int AP_WARPS = 8;
 
-template <int EPL>
-struct VecOf;
-template <>
-struct VecOf<2> { using T = uint32_t; };
-template <>
-struct VecOf<4> { using T = uint2; };
-template <>
-struct VecOf<8> { using T = uint4; };
-
-template <int EPL>
-__device__ __forceinline__ void widen(const typename VecOf<EPL>::T& v, float (&f)[EPL]) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+__device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < EPL / 2; ++j) {
+    for (int j = 0; j < 4; ++j) {
         f[2 * j] = __uint_as_float(w[j] << 16);
         f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
     }
 }
 
-// EPL E4M3 codes of f / scale
-template <int EPL>
-__device__ __forceinline__ void store_e4m3(char* dst, const float (&f)[EPL], float scale) {
-    if constexpr (EPL == 2) {
-        *reinterpret_cast<uint16_t*>(dst) =
-            __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(f[0], scale), __fdiv_rn(f[1], scale)), __NV_SATFINITE,
-                                     __NV_E4M3);
-    } else {
-        uint32_t w[EPL / 4];
+template <int N>
+struct Floats;
+template <>
+struct Floats<2> {
+    using T = float2;
+    static __device__ __forceinline__ float2 of(float v) { return make_float2(v, v); }
+};
+template <>
+struct Floats<4> {
+    using T = float4;
+    static __device__ __forceinline__ float4 of(float v) { return make_float4(v, v, v, v); }
+};
+
+// 8 E4M3 codes of f / scale
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale) {
+    float q[8];
 #pragma unroll
-        for (int j = 0; j < EPL / 4; ++j)
-            w[j] = pack_e4m3x4(__fdiv_rn(f[4 * j], scale), __fdiv_rn(f[4 * j + 1], scale),
-                               __fdiv_rn(f[4 * j + 2], scale), __fdiv_rn(f[4 * j + 3], scale));
-        if constexpr (EPL == 4) *reinterpret_cast<uint32_t*>(dst) = w[0];
-        else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[EPL / 4 - 1]);
-    }
+    for (int j = 0; j < 8; ++j) q[j] = __fdiv_rn(f[j], scale);
+    return make_uint2(pack_e4m3x4(q[0], q[1], q[2], q[3]), pack_e4m3x4(q[4], q[5], q[6], q[7]));
 }
 
 struct AppendArgs {
@@ -67,11 +64,13 @@ struct AppendArgs {
     int32_t* bad;
 };
 
-template <int EPL, int HPW, bool F8>
-__global__ void __launch_bounds__(AP_WARPS * 32) append_kernel(const AppendArgs a, const KvView c) {
-    constexpr int D = 32 * EPL;
-    using V = typename VecOf<EPL>::T;
-    const int lane = threadIdx.x & 31;
+// LPH lanes per head; SH: half of rot modulo 8 (where a dimension's rotation partner lies among
+// a lane's 8); KI: instructions' worth of heads per warp.
+template <int LPH, int SH, int KI, bool F8>
+__global__ void __launch_bounds__(AP_WARPS * 32, 3) append_kernel(const AppendArgs a, const KvView c) {
+    constexpr int D = 8 * LPH, HPI = 32 / LPH, HPW = KI * HPI;
+    constexpr int PS = D / 32, NP = 8 / PS;                        // dimensions per partial sum, partial sums per lane
+    const int lane = threadIdx.x & 31, L = lane % LPH, sub = lane / LPH;
     const int heads = a.n_q + 2 * c.n_kv;
     const int groups = (heads + HPW - 1) / HPW;
     const long long item = static_cast<long long>(blockIdx.x) * AP_WARPS + (threadIdx.x >> 5);
@@ -81,21 +80,42 @@ __global__ void __launch_bounds__(AP_WARPS * 32) append_kernel(const AppendArgs 
     const int nh = min(HPW, heads - h0);
 
     // the loads of the rows do not wait for the checks: every row t < T exists
-    const V* in = reinterpret_cast<const V*>(a.qkv + t * a.qkv_stride + static_cast<long long>(h0) * D);
-    V raw[HPW];
+    const uint16_t* in = a.qkv + t * a.qkv_stride + static_cast<long long>(h0 + sub) * D + L * 8;
+    uint4 raw[KI];
 #pragma unroll
-    for (int k = 0; k < HPW; ++k)
-        if (k < nh) raw[k] = in[k * 32 + lane];
+    for (int k = 0; k < KI; ++k)
+        if (k * HPI + sub < nh) raw[k] = *reinterpret_cast<const uint4*>(in + k * HPI * D);
+    const int p = a.rot > 0 ? a.pos[t] : 0;
 
     const int b = seq_of_row(c.q_start, c.B, t, lane);
     if (b < 0 || t >= c.q_start[b + 1]) return;                    // padding
     const bool counts = h0 <= a.n_q && a.n_q < h0 + nh;            // this warp has the first k head
-    int p = 0;
-    if (a.rot > 0) {
-        p = a.pos[t];
-        if (p < 0 || p >= a.max_pos) {
-            if (counts && lane == 0 && a.bad != nullptr) atomicAdd(a.bad, 1);
-            return;
+    if (a.rot > 0 && (p < 0 || p >= a.max_pos)) {
+        if (counts && lane == 0 && a.bad != nullptr) atomicAdd(a.bad, 1);
+        return;
+    }
+    const int i0 = L * 8, half = a.rot >> 1;   // first dimension of this lane
+    const float* cs = a.cos_sin + static_cast<long long>(p) * a.rot;
+    float co[8], sn[8];
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {             // PS dimensions rotate alike
+        const int d = i0 + n * PS;
+        const bool turn = d < a.rot && h0 < a.n_q + c.n_kv;
+        const int at = d < half ? d : d - half;
+        const float sign = d < half ? -1.0f : 1.0f;
+        using F = typename Floats<PS < 4 ? 2 : 4>::T;
+#pragma unroll
+        for (int j = 0; j < PS; j += (PS < 4 ? 2 : 4)) {
+            F x = Floats<PS < 4 ? 2 : 4>::of(1.0f), y = Floats<PS < 4 ? 2 : 4>::of(0.0f);
+            if (turn) {
+                x = *reinterpret_cast<const F*>(cs + at + j);
+                y = *reinterpret_cast<const F*>(cs + half + at + j);
+            }
+#pragma unroll
+            for (int e = 0; e < (PS < 4 ? 2 : 4); ++e) {
+                co[n * PS + j + e] = reinterpret_cast<const float*>(&x)[e];
+                sn[n * PS + j + e] = sign * reinterpret_cast<const float*>(&y)[e];
+            }
         }
     }
     long long slot = -1;
@@ -104,90 +124,83 @@ __global__ void __launch_bounds__(AP_WARPS * 32) append_kernel(const AppendArgs 
         if (s.ok) slot = slot_offset(c, b, s.ctx + (t - s.row0), 0);
         if (slot < 0 && counts && lane == 0 && a.bad != nullptr) atomicAdd(a.bad, 1);
     }
-
-    const int half = a.rot >> 1;
-    const int i0 = lane * EPL;                 // first dimension of this lane
-    const int lane_off = half / EPL;           // rotation partners are this many lanes apart
-    const int src = (i0 < half) ? lane + lane_off : (i0 < a.rot ? lane - lane_off : lane);
-    float co[EPL], sn[EPL];
+    // norm weights as they are stored (registers decide how many warps are in flight)
+    uint4 wq = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u), wk = wq;   // 1.0
+    if (a.q_w != nullptr && h0 < a.n_q) wq = reinterpret_cast<const uint4*>(a.q_w)[L];
+    if (a.k_w != nullptr && h0 + nh > a.n_q) wk = reinterpret_cast<const uint4*>(a.k_w)[L];
+    // dimension d's partner is d + half in the first half and d - half in the second: element
+    // (j + SH) % 8 of the lane that holds it
+    int src[NP];
+    bool turns[NP];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        co[j] = 1.0f;
-        sn[j] = 0.0f;
+    for (int n = 0; n < NP; ++n) {
+        const int d = i0 + n * PS;
+        turns[n] = d < a.rot;
+        src[n] = sub * LPH + (d < half ? (d + half) >> 3 : (turns[n] ? (d - half) >> 3 : L));
     }
-    if (i0 < a.rot && h0 < a.n_q + c.n_kv) {
-        const float* cs = a.cos_sin + static_cast<long long>(p) * a.rot + (i0 < half ? i0 : i0 - half);
-        const float sign = i0 < half ? -1.0f : 1.0f;
+
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            co[j] = cs[j];
-            sn[j] = sign * cs[half + j];
+    for (int k = 0; k < KI; ++k) {
+        const int h = h0 + k * HPI + sub;
+        if (k * HPI >= nh) break;                                  // warp-uniform
+        const bool is_q = h < a.n_q, is_v = h >= a.n_q + c.n_kv, real = h < heads;
+        float v[8];
+        widen8(real ? raw[k] : make_uint4(0, 0, 0, 0), v);
+        // (all lanes take part in the butterfly, whatever their heads)
+        float ss[NP];
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            ss[n] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < PS; ++j) ss[n] = fmaf(v[n * PS + j], v[n * PS + j], ss[n]);
         }
-    }
-    float wq[EPL], wk[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) wq[j] = wk[j] = 1.0f;
-    if (a.q_w != nullptr && h0 < a.n_q) widen<EPL>(reinterpret_cast<const V*>(a.q_w)[lane], wq);
-    if (a.k_w != nullptr && h0 + nh > a.n_q) widen<EPL>(reinterpret_cast<const V*>(a.k_w)[lane], wk);
-
+        for (int off = LPH / 2; off > 0; off >>= 1)
 #pragma unroll
-    for (int k = 0; k < HPW; ++k) {
-        if (k >= nh) break;                                        // warp-uniform
-        const int h = h0 + k;
-        if (h >= a.n_q + c.n_kv) {                                 // a v head
-            if (slot < 0) continue;
-            char* dst = c.v + slot + (h - a.n_q - c.n_kv) * c.head_b;
-            if constexpr (F8) {
-                float v[EPL];
-                widen<EPL>(raw[k], v);
-                store_e4m3<EPL>(dst + lane * EPL, v, c.v_scale);
-            } else {
-                reinterpret_cast<V*>(dst)[lane] = raw[k];
-            }
+            for (int n = 0; n < NP; ++n) ss[n] += __shfl_xor_sync(0xFFFFFFFFu, ss[n], off);
+#pragma unroll
+        for (int off = NP / 2; off > 0; off >>= 1)
+#pragma unroll
+            for (int n = 0; n < off; ++n) ss[n] += ss[n + off];
+        const float r = (is_q ? a.q_w : a.k_w) != nullptr ? rsqrtf(ss[0] / D + a.eps) : 1.0f;
+        float u[8], y[8], w[8];
+        widen8(is_q ? wq : wk, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = v[j] * r * w[j];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // every lane offers its element (j + SH) % 8 and takes its partner's
+            const float partner = __shfl_sync(0xFFFFFFFFu, u[(j + SH) & 7], src[j / PS]);
+            // dimensions that do not rotate pass through whatever their value (0 * infinity)
+            y[j] = turns[j / PS] ? u[j] * co[j] + partner * sn[j] : u[j];
+        }
+        if (!real || (!is_q && slot < 0)) continue;
+        const uint4 out = is_v ? raw[k]
+                               : make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                            pack_bf16x2(y[6], y[7]));
+        if (is_q) {
+            *reinterpret_cast<uint4*>(a.q_out + t * a.q_stride + static_cast<long long>(h) * D + i0) = out;
             continue;
         }
-        const bool is_q = h < a.n_q;
-        if (!is_q && slot < 0) continue;
-        float v[EPL];
-        widen<EPL>(raw[k], v);
-        const bool norm = (is_q ? a.q_w : a.k_w) != nullptr;
-        float r = 1.0f;
-        if (norm) {
-            float ss = 0.0f;
+        char* dst = (is_v ? c.v + (h - a.n_q - c.n_kv) * c.head_b : c.k + (h - a.n_q) * c.head_b) + slot;
+        if constexpr (F8) {
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) ss = fmaf(v[j], v[j], ss);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
-            r = rsqrtf(ss / D + a.eps);
-        }
-        float y[EPL];
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            const float u = v[j] * r * (is_q ? wq[j] : wk[j]);
-            const float partner = __shfl_sync(0xFFFFFFFFu, u, src);
-            // dimensions that do not rotate pass through whatever their value (0 * infinity)
-            y[j] = i0 < a.rot ? u * co[j] + partner * sn[j] : u;
-        }
-        if (!is_q && F8) {
-            store_e4m3<EPL>(c.k + slot + (h - a.n_q) * c.head_b + lane * EPL, y, c.k_scale);
+            for (int j = 0; j < 8; ++j) y[j] = is_v ? v[j] : y[j];
+            *reinterpret_cast<uint2*>(dst + i0) = codes8(y, is_v ? c.v_scale : c.k_scale);
         } else {
-            uint32_t o[EPL / 2];
-#pragma unroll
-            for (int j = 0; j < EPL; j += 2) o[j >> 1] = pack_bf16x2(y[j], y[j + 1]);
-            V* dst = is_q ? reinterpret_cast<V*>(a.q_out + t * a.q_stride + static_cast<long long>(h) * D)
-                          : reinterpret_cast<V*>(c.k + slot + (h - a.n_q) * c.head_b);
-            dst[lane] = *reinterpret_cast<const V*>(o);
+            *reinterpret_cast<uint4*>(dst + i0 * 2) = out;
         }
     }
 }
 
-template <int EPL>
-void append_epl(const AppendArgs& a, const KvView& c, bool f8, cudaStream_t st) {
-    constexpr int HPW = 8;
+template <int LPH, int SH>
+void append_sh(const AppendArgs& a, const KvView& c, bool f8, cudaStream_t st) {
+    constexpr int KI = LPH == 32 ? 8 : 4;      // heads per warp: 8, or 16 of 64 dimensions
+    constexpr int HPW = KI * (32 / LPH);
     const long long items = static_cast<long long>(a.T) * ((a.n_q + 2 * c.n_kv + HPW - 1) / HPW);
     const unsigned blocks = static_cast<unsigned>((items + AP_WARPS - 1) / AP_WARPS);
-    if (f8) append_kernel<EPL, HPW, true><<<blocks, AP_WARPS * 32, 0, st>>>(a, c);
-    else append_kernel<EPL, HPW, false><<<blocks, AP_WARPS * 32, 0, st>>>(a, c);
+    if (f8) append_kernel<LPH, SH, KI, true><<<blocks, AP_WARPS * 32, 0, st>>>(a, c);
+    else append_kernel<LPH, SH, KI, false><<<blocks, AP_WARPS * 32, 0, st>>>(a, c);
 }
 
 // Compaction. A thread owns one 16-byte column of one (layer, K or V, head) of a
@@ -195,7 +208,8 @@ void append_epl(const AppendArgs& a, const KvView& c, bool f8, cudaStream_t st) 
 // front of their destinations and nobody else touches its column, so reading a few
 // tokens ahead of the writes keeps the move in place and free of barriers.
 constexpr int CP_THREADS = 256;
-constexpr int CP_AHEAD = 8;
+constexpr int CP_AHEAD = 4;              // tokens read before the first of them is written
+constexpr int CP_COLS = 2;               // columns per thread: two loads in flight for each token ahead
 
 __global__ void __launch_bounds__(CP_THREADS) compact_kernel(const KvView c, int n_layers, long long layer_b,
                                                              const int32_t* __restrict__ accepted, int max_accept,
@@ -230,25 +244,33 @@ __global__ void __launch_bounds__(CP_THREADS) compact_kernel(const KvView c, int
         return;
     }
     const long long cols = static_cast<long long>(n_layers) * 2 * c.n_kv * row_chunks;
-    const long long col = static_cast<long long>(blockIdx.x) * CP_THREADS + threadIdx.x;
-    if (col >= cols) return;
-    const int chunk = static_cast<int>(col % row_chunks);
-    long long rest = col / row_chunks;
-    const int h = static_cast<int>(rest % c.n_kv);
-    rest /= c.n_kv;
-    char* base = ((rest & 1) ? c.v : c.k) + (rest >> 1) * layer_b + h * c.head_b + chunk * 16;
+    char* base[CP_COLS];
+#pragma unroll
+    for (int q = 0; q < CP_COLS; ++q) {
+        const long long col = (static_cast<long long>(blockIdx.x) * CP_COLS + q) * CP_THREADS + threadIdx.x;
+        const int chunk = static_cast<int>(col % row_chunks);
+        long long rest = col / row_chunks;
+        const int h = static_cast<int>(rest % c.n_kv);
+        rest /= c.n_kv;
+        base[q] = col < cols ? ((rest & 1) ? c.v : c.k) + (rest >> 1) * layer_b + h * c.head_b + chunk * 16 : nullptr;
+    }
     for (int i0 = 0; i0 < n; i0 += CP_AHEAD) {
-        uint4 x[CP_AHEAD];
+        uint4 x[CP_COLS][CP_AHEAD];
 #pragma unroll
         for (int j = 0; j < CP_AHEAD; ++j) {
             const int i = i0 + j;
-            if (i < n && cp_off[i] != cp_off[max_accept + i]) x[j] = *reinterpret_cast<const uint4*>(base + cp_off[i]);
+            if (i >= n || cp_off[i] == cp_off[max_accept + i]) continue;
+#pragma unroll
+            for (int q = 0; q < CP_COLS; ++q)
+                if (base[q] != nullptr) x[q][j] = *reinterpret_cast<const uint4*>(base[q] + cp_off[i]);
         }
 #pragma unroll
         for (int j = 0; j < CP_AHEAD; ++j) {
             const int i = i0 + j;
-            if (i < n && cp_off[i] != cp_off[max_accept + i])
-                *reinterpret_cast<uint4*>(base + cp_off[max_accept + i]) = x[j];
+            if (i >= n || cp_off[i] == cp_off[max_accept + i]) continue;
+#pragma unroll
+            for (int q = 0; q < CP_COLS; ++q)
+                if (base[q] != nullptr) *reinterpret_cast<uint4*>(base[q] + cp_off[max_accept + i]) = x[q][j];
         }
     }
 }
@@ -260,9 +282,13 @@ cudaError_t launch_append(const KvView& c, int head_dim, bool f8, int T, int n_q
                           const float* cos_sin, uint16_t* q_out, long long q_stride, int32_t* bad, cudaStream_t st) {
     ProfileScope ps("qk_norm_rope_append", st);
     AppendArgs a{T, n_q, rot, max_pos, eps, qkv, qkv_stride, q_stride, pos, q_w, k_w, cos_sin, q_out, bad};
-    if (head_dim == 64) append_epl<2>(a, c, f8, st);
-    else if (head_dim == 128) append_epl<4>(a, c, f8, st);
-    else append_epl<8>(a, c, f8, st);
+    const int sh = (rot / 2) % 8;              // a multiple of head_dim / 32
+    if (head_dim == 256) append_sh<32, 0>(a, c, f8, st);
+    else if (head_dim == 128) sh == 0 ? append_sh<16, 0>(a, c, f8, st) : append_sh<16, 4>(a, c, f8, st);
+    else if (sh == 0) append_sh<8, 0>(a, c, f8, st);
+    else if (sh == 2) append_sh<8, 2>(a, c, f8, st);
+    else if (sh == 4) append_sh<8, 4>(a, c, f8, st);
+    else append_sh<8, 6>(a, c, f8, st);
     note_launch();
     return cudaGetLastError();
 }
@@ -272,7 +298,7 @@ cudaError_t launch_compact(const KvView& c, int row_bytes, int n_layers, long lo
     ProfileScope ps("kv_compact", st);
     const int row_chunks = row_bytes / 16;
     const long long cols = static_cast<long long>(n_layers) * 2 * c.n_kv * row_chunks;
-    const dim3 grid(static_cast<unsigned>((cols + CP_THREADS - 1) / CP_THREADS), c.B);
+    const dim3 grid(static_cast<unsigned>((cols + CP_THREADS * CP_COLS - 1) / (CP_THREADS * CP_COLS)), c.B);
     compact_kernel<<<grid, CP_THREADS, 2 * sizeof(long long) * max_accept, st>>>(c, n_layers, layer_b, accepted,
                                                                                  max_accept, n_accepted, row_chunks, bad);
     note_launch();

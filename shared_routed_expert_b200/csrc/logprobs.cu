@@ -30,7 +30,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int LP_THREADS = 512;
+constexpr int LP_THREADS = 256;
 constexpr int LP_WARPS = LP_THREADS / 32;
 constexpr int kU = 4;                    // 16-byte vectors per group
 constexpr int kG = 16;                   // runs of groups per thread
@@ -62,6 +62,29 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// pairs of fp32 in one register pair
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 // a thread's sums against its reference (its maximum, or 0 while everything is -infinity)
@@ -162,7 +185,7 @@ __device__ __forceinline__ unsigned long long block_max(LpShared& sh, unsigned l
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(int V, const char* __restrict__ logits,
+__global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(int V, const char* __restrict__ logits,
                                                               long long row_b, const int32_t* __restrict__ targets,
                                                               int top_n, float* __restrict__ logprobs,
                                                               float* __restrict__ entropy, int32_t* __restrict__ top_ids,
@@ -215,12 +238,35 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(int V, const ch
             rest.l = l * a;
         }
         float l = 0.f, tt = 0.f;
+        if constexpr (n % 4 == 0) {
+            // pairs, one instruction each; the difference first: exact near the maximum
+            const uint64_t r2 = pair2(-ref, -ref), c2 = pair2(kLog2e, kLog2e);
+            uint64_t l2[2] = {0, 0}, t2[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < n; ++j) {
-            const float d = (f[j] - ref) * kLog2e;                 // the difference first: exact near the maximum
-            const float e = exp2_fast(d);
-            l += e;
-            tt = fmaf(e, fmaxf(d, -1.0e30f), tt);                  // -infinity: 0 * a finite number
+            for (int j = 0; j < n; j += 2) {
+                const uint64_t d2 = mul2(add2(pair2(f[j], f[j + 1]), r2), c2);
+                float da, db;
+                unpair2(d2, da, db);
+                const uint64_t e2 = pair2(exp2_fast(da), exp2_fast(db));
+                l2[(j >> 1) & 1] = add2(l2[(j >> 1) & 1], e2);
+                t2[(j >> 1) & 1] = fma2(e2, d2, t2[(j >> 1) & 1]);
+            }
+            float x, y;
+            unpair2(add2(l2[0], l2[1]), x, y);
+            l = x + y;
+            unpair2(add2(t2[0], t2[1]), x, y);
+            tt = x + y;
+        }
+        if (n % 4 != 0 || tt != tt) {
+            // one by one, with -infinity (where 0 * d is not 0) looked after
+            l = tt = 0.f;
+#pragma unroll
+            for (int j = 0; j < n; ++j) {
+                const float d = (f[j] - ref) * kLog2e;
+                const float e = exp2_fast(d);
+                l += e;
+                tt = fmaf(e, fmaxf(d, -1.0e30f), tt);
+            }
         }
         if (gm > m) {
             best.l = l;
@@ -243,22 +289,29 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(int V, const ch
         run = m;
     }
     int run_i = 0;
-    for (int g = 0; g < groups; ++g) {
-        const int v0 = v_lo + g * (kU * LP_THREADS) + tid;
-        uint4 w[kU];
+    uint4 w[kU];
+    auto fetch = [&](int g) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int v = v0 + u * LP_THREADS;
-            if (v < v_hi) w[u] = row.vec(v);
+            const int v = v_lo + g * (kU * LP_THREADS) + tid + u * LP_THREADS;
+            if (g < groups && v < v_hi) w[u] = row.vec(v);
             else w[u] = BF16 ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
                              : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);   // -infinity
         }
+    };
+    fetch(0);
+    for (int g = 0; g < groups; ++g) {
         float f[R::GE];
 #pragma unroll
         for (int u = 0; u < kU; ++u) R::widen(w[u], f + u * R::VE);
-        float gm = f[0];
+        fetch(g + 1);                                              // on its way while this group is summed
+        float gm = f[0], gm2 = f[1];
 #pragma unroll
-        for (int j = 1; j < R::GE; ++j) gm = fmaxf(gm, f[j]);
+        for (int j = 2; j < R::GE; j += 4) {
+            gm = fmaxf(fmaxf(gm, f[j]), f[j + 1]);
+            if (j + 2 < R::GE) gm2 = fmaxf(fmaxf(gm2, f[j + 2]), f[j + 3]);
+        }
+        gm = fmaxf(gm, gm2);
         account(f, gm, g);
         run = fmaxf(run, gm);
         if ((g + 1) % per_run == 0 || g + 1 == groups) {
