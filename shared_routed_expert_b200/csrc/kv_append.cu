@@ -67,7 +67,7 @@ struct AppendArgs {
 // LPH lanes per head; SH: half of rot modulo 8 (where a dimension's rotation partner lies among
 // a lane's 8); KI: instructions' worth of heads per warp.
 template <int LPH, int SH, int KI, bool F8>
-__global__ void __launch_bounds__(AP_WARPS * 32, 3) append_kernel(const AppendArgs a, const KvView c) {
+__global__ void __launch_bounds__(AP_WARPS * 32, 4) append_kernel(const AppendArgs a, const KvView c) {
     constexpr int D = 8 * LPH, HPI = 32 / LPH, HPW = KI * HPI;
     constexpr int PS = D / 32, NP = 8 / PS;                        // dimensions per partial sum, partial sums per lane
     const int lane = threadIdx.x & 31, L = lane % LPH, sub = lane / LPH;
@@ -139,14 +139,8 @@ __global__ void __launch_bounds__(AP_WARPS * 32, 3) append_kernel(const AppendAr
         src[n] = sub * LPH + (d < half ? (d + half) >> 3 : (turns[n] ? (d - half) >> 3 : L));
     }
 
-#pragma unroll
-    for (int k = 0; k < KI; ++k) {
-        const int h = h0 + k * HPI + sub;
-        if (k * HPI >= nh) break;                                  // warp-uniform
-        const bool is_q = h < a.n_q, is_v = h >= a.n_q + c.n_kv, real = h < heads;
-        float v[8];
-        widen8(real ? raw[k] : make_uint4(0, 0, 0, 0), v);
-        // (all lanes take part in the butterfly, whatever their heads)
+    // u = v r w of 8 dimensions, r from the head's mean square
+    auto normed = [&](const float (&v)[8], const float (&w)[8], bool norm, float (&u)[8]) {
         float ss[NP];
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
@@ -162,20 +156,52 @@ __global__ void __launch_bounds__(AP_WARPS * 32, 3) append_kernel(const AppendAr
         for (int off = NP / 2; off > 0; off >>= 1)
 #pragma unroll
             for (int n = 0; n < off; ++n) ss[n] += ss[n + off];
-        const float r = (is_q ? a.q_w : a.k_w) != nullptr ? rsqrtf(ss[0] / D + a.eps) : 1.0f;
-        float u[8], y[8], w[8];
-        widen8(is_q ? wq : wk, w);
+        const float r = norm ? rsqrtf(ss[0] / D + a.eps) : 1.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = v[j] * r * w[j];
+    };
+    // every lane offers its element (j + SH) % 8 and takes its partner's
+    auto partner = [&](const float (&u)[8], int j) { return __shfl_sync(0xFFFFFFFFu, u[(j + SH) & 7], src[j / PS]); };
+
+    if (h0 + HPW <= a.n_q && a.q_w != nullptr) {
+        // q heads alone (most warps): nothing to tell apart
+        float w[8];
+        widen8(wq, w);
+        uint16_t* dst = a.q_out + t * a.q_stride + static_cast<long long>(h0 + sub) * D + i0;
+#pragma unroll
+        for (int k = 0; k < KI; ++k) {
+            float v[8], u[8], y[8];
+            widen8(raw[k], v);
+            normed(v, w, true, u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = u[j] * co[j] + partner(u, j) * sn[j];
+            *reinterpret_cast<uint4*>(dst + k * HPI * D) =
+                make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int k = 0; k < KI; ++k) {
+        const int h = h0 + k * HPI + sub;
+        if (k * HPI >= nh) break;                                  // warp-uniform
+        const bool is_q = h < a.n_q, is_v = h >= a.n_q + c.n_kv, real = h < heads;
+        uint4 x = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < KI; ++q)
+            if (q == k && real) x = raw[q];
+        float v[8], u[8], y[8], w[8];
+        widen8(x, v);
+        widen8(is_q ? wq : wk, w);
+        // (all lanes take part in the shuffles, whatever their heads)
+        normed(v, w, (is_q ? a.q_w : a.k_w) != nullptr, u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            // every lane offers its element (j + SH) % 8 and takes its partner's
-            const float partner = __shfl_sync(0xFFFFFFFFu, u[(j + SH) & 7], src[j / PS]);
+            const float o = partner(u, j);
             // dimensions that do not rotate pass through whatever their value (0 * infinity)
-            y[j] = turns[j / PS] ? u[j] * co[j] + partner * sn[j] : u[j];
+            y[j] = turns[j / PS] ? u[j] * co[j] + o * sn[j] : u[j];
         }
         if (!real || (!is_q && slot < 0)) continue;
-        const uint4 out = is_v ? raw[k]
+        const uint4 out = is_v ? x
                                : make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
                                             pack_bf16x2(y[6], y[7]));
         if (is_q) {
@@ -193,14 +219,23 @@ __global__ void __launch_bounds__(AP_WARPS * 32, 3) append_kernel(const AppendAr
     }
 }
 
-template <int LPH, int SH>
-void append_sh(const AppendArgs& a, const KvView& c, bool f8, cudaStream_t st) {
-    constexpr int KI = LPH == 32 ? 8 : 4;      // heads per warp: 8, or 16 of 64 dimensions
+template <int LPH, int SH, int KI>
+void append_ki(const AppendArgs& a, const KvView& c, bool f8, cudaStream_t st) {
     constexpr int HPW = KI * (32 / LPH);
     const long long items = static_cast<long long>(a.T) * ((a.n_q + 2 * c.n_kv + HPW - 1) / HPW);
     const unsigned blocks = static_cast<unsigned>((items + AP_WARPS - 1) / AP_WARPS);
     if (f8) append_kernel<LPH, SH, KI, true><<<blocks, AP_WARPS * 32, 0, st>>>(a, c);
     else append_kernel<LPH, SH, KI, false><<<blocks, AP_WARPS * 32, 0, st>>>(a, c);
+}
+
+template <int LPH, int SH>
+void append_sh(const AppendArgs& a, const KvView& c, bool f8, cudaStream_t st) {
+    constexpr int KI = LPH == 32 ? 8 : 4;      // heads per warp: 8, or 16 of 64 dimensions
+    // a decode batch that the SMs hold at once takes half as many heads a warp: a shorter chain
+    // (1 token of 112 heads 2.9 against 3.4 us, 64 tokens 4.1 against 4.8 us), while more heads
+    // share what is looked up per token in a prefill chunk (5949 tokens 78 against 100 us)
+    if (static_cast<long long>(a.T) * (a.n_q + 2 * c.n_kv) <= 16384) append_ki<LPH, SH, KI / 2>(a, c, f8, st);
+    else append_ki<LPH, SH, KI>(a, c, f8, st);
 }
 
 // Compaction. A thread owns one 16-byte column of one (layer, K or V, head) of a
