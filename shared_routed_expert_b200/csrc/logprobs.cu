@@ -39,7 +39,7 @@ constexpr int kCand = 512;               // candidates a block ranks
 constexpr int kMaxC = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-static_assert(kMaxC * kTop <= LP_THREADS && kMaxC * kTop <= kCand, "the join has a thread and a place per alternative");
+static_assert(kMaxC <= LP_WARPS && kTop == 32, "the join has a warp per slice and a lane per alternative");
 
 // order-preserving key: larger values have larger keys, NaN the largest, -0 = +0
 __device__ __forceinline__ uint32_t value_key(float x) {
@@ -126,6 +126,7 @@ struct LpShared {
     unsigned long long cand[kCand];
     unsigned long long top[kTop];        // this block's alternatives, best first
     unsigned long long warp_top[LP_WARPS][32];
+    uint32_t warp_key[LP_WARPS][32];
     float red[LP_WARPS][4];
     float4 part[kMaxC];                  // rank 0: the slices' m, l, t, bad
     float4 sums;                         // this block's maximum, its sums without one maximum, and whether
@@ -133,38 +134,40 @@ struct LpShared {
     int n_cand;
 };
 
-// The 32 largest of the block's 512 keys (one per thread), sorted descending, to
-// out[32] (shared). Every warp sorts its lanes, then lists are merged pairwise.
-__device__ __forceinline__ unsigned long long sort_desc_warp(unsigned long long k, int lane) {
+// Sorted lists of 32 over a warp's lanes, largest first.
+template <typename K>
+__device__ __forceinline__ K sort_desc_warp(K k, int lane) {
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1) {
 #pragma unroll
         for (int j = size >> 1; j > 0; j >>= 1) {
-            const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, k, j);
+            const K o = __shfl_xor_sync(0xFFFFFFFFu, k, j);
             const bool first = (lane & j) == 0, desc = (lane & size) == 0 || size == 32;
             k = (first == desc) ? (k > o ? k : o) : (k < o ? k : o);
         }
     }
     return k;
 }
-// a, b sorted descending over the lanes -> the 32 largest of both, sorted descending
-__device__ __forceinline__ unsigned long long merge_desc_warp(unsigned long long a, unsigned long long b, int lane) {
-    const unsigned long long r = __shfl_sync(0xFFFFFFFFu, b, 31 - lane);
-    unsigned long long k = a > r ? a : r;                          // bitonic, holds the 32 largest
+// a, b sorted -> the 32 largest of both, sorted
+template <typename K>
+__device__ __forceinline__ K merge_desc_warp(K a, K b, int lane) {
+    const K r = __shfl_sync(0xFFFFFFFFu, b, 31 - lane);
+    K k = a > r ? a : r;                                           // bitonic, holds the 32 largest
 #pragma unroll
     for (int j = 16; j > 0; j >>= 1) {
-        const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, k, j);
+        const K o = __shfl_xor_sync(0xFFFFFFFFu, k, j);
         k = ((lane & j) == 0) ? (k > o ? k : o) : (k < o ? k : o);
     }
     return k;
 }
-__device__ __forceinline__ void block_top32(LpShared& sh, unsigned long long key, int warp, int lane) {
-    sh.warp_top[warp][lane] = sort_desc_warp(key, lane);
+// the 32 largest of the block's sorted lists (one per warp), to lists[0]
+template <typename K>
+__device__ __forceinline__ void merge_block(K (*lists)[32], K k, int warp, int lane) {
+    lists[warp][lane] = k;
     __syncthreads();
 #pragma unroll
     for (int w = LP_WARPS / 2; w > 0; w >>= 1) {
-        if (warp < w)
-            sh.warp_top[warp][lane] = merge_desc_warp(sh.warp_top[warp][lane], sh.warp_top[warp + w][lane], lane);
+        if (warp < w) lists[warp][lane] = merge_desc_warp(lists[warp][lane], lists[warp + w][lane], lane);
         __syncthreads();
     }
 }
@@ -211,13 +214,6 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(int V, const ch
     const int per_run = max(1, (groups + kG - 1) / kG);
     if (tid == 0) {
         sh.n_cand = 0;
-    }
-
-    int target = -1;
-    float x_target = 0.f;
-    if (rank == 0 && tid == 0 && logprobs != nullptr) {
-        target = targets[t];
-        if (target >= 0 && target < V) x_target = row.at(target);
     }
 
     // ---- one pass: m, rest (without the best group), best
@@ -300,6 +296,12 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(int V, const ch
         }
     };
     fetch(0);
+    int target = -1;
+    float x_target = 0.f;
+    if (rank == 0 && tid == 0 && logprobs != nullptr) {
+        target = targets[t];
+        if (target >= 0 && target < V) x_target = row.at(target);
+    }
     for (int g = 0; g < groups; ++g) {
         float f[R::GE];
 #pragma unroll
@@ -344,16 +346,107 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(int V, const ch
         if (hw) owner = w * 32 + __ffs(hw) - 1;
     }
     const float bref = bm == -INFINITY ? 0.0f : bm;
+    uint4 again[kU];                                               // the owner's best group, on its way while the alternatives are found
+    if (tid == owner && best_g >= 0) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int v = v_lo + best_g * (kU * LP_THREADS) + tid + u * LP_THREADS;
+            again[u] = v < v_hi ? row.vec(v) : make_uint4(0, 0, 0, 0);
+        }
+    }
+
+    // ---- this block's alternatives (rows with NaN or +infinity: see below)
+    const bool odd = __syncthreads_or(!(rest.l + best.l < INFINITY)) || bm == INFINITY;
+    if (top_n > 0) {
+        bool rounds = odd;
+        if (!rounds) {
+            // the n-th largest of the threads' maxima
+            merge_block(sh.warp_key, sort_desc_warp(value_key(m), lane), warp, lane);
+            const float tau = key_value(sh.warp_key[0][top_n - 1]);
+            auto offer = [&](float x, int id) {
+                const int i = atomicAdd(&sh.n_cand, 1);
+                if (i < kCand) sh.cand[i] = pair_key(x, id);
+            };
+            if (m >= tau) {
+                if (scalar >= 0) {
+                    const float x = row.at(scalar);
+                    if (x >= tau) offer(x, scalar);
+                }
+                for (int r = 0; r < run_i; ++r) {
+                    if (groups == 0 || !(sh.run_max[r][tid] >= tau)) continue;
+                    for (int g = r * per_run; g < min(groups, (r + 1) * per_run); ++g) {
+                        uint4 q[kU];
+#pragma unroll
+                        for (int u = 0; u < kU; ++u) {
+                            const int v = v_lo + g * (kU * LP_THREADS) + tid + u * LP_THREADS;
+                            if (v < v_hi) q[u] = row.vec(v);
+                        }
+#pragma unroll
+                        for (int u = 0; u < kU; ++u) {
+                            const int v = v_lo + g * (kU * LP_THREADS) + tid + u * LP_THREADS;
+                            float f[R::VE];
+                            R::widen(q[u], f);
+                            unsigned hit = 0;
+#pragma unroll
+                            for (int j = 0; j < R::VE; ++j) hit |= (f[j] >= tau ? 1u : 0u) << j;
+                            if (v >= v_hi) hit = 0;
+                            while (hit) {
+                                const int j = __ffs(hit) - 1;
+                                hit &= hit - 1;
+                                const int id = row.head + v * R::VE + j;
+                                offer(row.at(id), id);
+                            }
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+            const int n = sh.n_cand;
+            rounds = n > kCand;
+            if (!rounds) {
+                if (tid < kTop) sh.top[tid] = 0;
+                __syncthreads();
+                for (int i = tid; i < n; i += LP_THREADS) {
+                    const unsigned long long k = sh.cand[i];
+                    int r = 0;
+#pragma unroll 8
+                    for (int j = 0; j < n; ++j) r += sh.cand[j] > k;
+                    if (r < top_n) sh.top[r] = k;
+                }
+            }
+        }
+        if (rounds) {
+            if (tid < kTop) sh.top[tid] = 0;
+            unsigned long long last = ~0ull;
+            for (int i = 0; i < top_n; ++i) {
+                unsigned long long k = 0;
+                auto look = [&](float x, int id) {
+                    const unsigned long long p = pair_key(x, id);
+                    if ((p < last || i == 0) && p > k) k = p;
+                };
+                if (scalar >= 0) look(row.at(scalar), scalar);
+                for (int v = v_lo + tid; v < v_hi; v += LP_THREADS) {
+                    float f[R::VE];
+                    R::widen(row.vec(v), f);
+#pragma unroll
+                    for (int j = 0; j < R::VE; ++j) look(f[j], row.head + v * R::VE + j);
+                }
+                last = block_max(sh, k, warp, lane);
+                if (tid == 0) sh.top[i] = last;
+            }
+        }
+    }
+
+    // ---- the block's sums, the owner's best group without the first occurrence of the maximum
     if (tid == owner) {
-        // its best group again, without the first occurrence of the maximum
         best.l = best.t = 0.f;
         if (best_g >= 0) {
             bool out = false;
+#pragma unroll
             for (int u = 0; u < kU; ++u) {
-                const int v = v_lo + best_g * (kU * LP_THREADS) + tid + u * LP_THREADS;
-                if (v >= v_hi) continue;
+                if (v_lo + best_g * (kU * LP_THREADS) + tid + u * LP_THREADS >= v_hi) continue;
                 float f[R::VE];
-                R::widen(row.vec(v), f);
+                R::widen(again[u], f);
 #pragma unroll
                 for (int j = 0; j < R::VE; ++j) {
                     if (!out && f[j] == bm) {
@@ -393,89 +486,28 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(int V, const ch
             l += sh.red[w][2];
             tt += sh.red[w][3];
         }
-        sh.sums = make_float4(bm, l, tt, !(l < INFINITY) || bm == INFINITY ? 1.f : 0.f);
+        sh.sums = make_float4(bm, l, tt, odd ? 1.f : 0.f);
     }
     __syncthreads();
-
-    // ---- this block's alternatives
-    if (top_n > 0) {
-        bool rounds = sh.sums.w != 0.f;
-        if (!rounds) {
-            // the n-th largest of the threads' maxima (by value alone: key << 32)
-            block_top32(sh, static_cast<unsigned long long>(value_key(m)) << 32, warp, lane);
-            const float tau = key_value(static_cast<uint32_t>(sh.warp_top[0][top_n - 1] >> 32));
-            __syncthreads();
-            auto offer = [&](float x, int id) {
-                if (x >= tau) {
-                    const int i = atomicAdd(&sh.n_cand, 1);
-                    if (i < kCand) sh.cand[i] = pair_key(x, id);
-                }
-            };
-            if (m >= tau) {
-                if (scalar >= 0) offer(row.at(scalar), scalar);
-                for (int r = 0; r < run_i; ++r) {
-                    if (groups == 0 || !(sh.run_max[r][tid] >= tau)) continue;
-                    for (int g = r * per_run; g < min(groups, (r + 1) * per_run); ++g) {
-#pragma unroll
-                        for (int u = 0; u < kU; ++u) {
-                            const int v = v_lo + g * (kU * LP_THREADS) + tid + u * LP_THREADS;
-                            if (v >= v_hi) continue;
-                            float f[R::VE];
-                            R::widen(row.vec(v), f);
-#pragma unroll
-                            for (int j = 0; j < R::VE; ++j) offer(f[j], row.head + v * R::VE + j);
-                        }
-                    }
-                }
-            }
-            __syncthreads();
-            const int n = sh.n_cand;
-            rounds = n > kCand;
-            if (!rounds) {
-                if (tid < kTop) sh.top[tid] = 0;
-                __syncthreads();
-                for (int i = tid; i < n; i += LP_THREADS) {
-                    const unsigned long long k = sh.cand[i];
-                    int r = 0;
-                    for (int j = 0; j < n; ++j) r += sh.cand[j] > k;
-                    if (r < top_n) sh.top[r] = k;
-                }
-            }
-        }
-        if (rounds) {
-            unsigned long long last = ~0ull;
-            for (int i = 0; i < top_n; ++i) {
-                unsigned long long k = 0;
-                auto look = [&](float x, int id) {
-                    const unsigned long long p = pair_key(x, id);
-                    if ((p < last || i == 0) && p > k) k = p;
-                };
-                if (scalar >= 0) look(row.at(scalar), scalar);
-                for (int v = v_lo + tid; v < v_hi; v += LP_THREADS) {
-                    float f[R::VE];
-                    R::widen(row.vec(v), f);
-#pragma unroll
-                    for (int j = 0; j < R::VE; ++j) look(f[j], row.head + v * R::VE + j);
-                }
-                last = block_max(sh, k, warp, lane);
-                if (tid == 0) sh.top[i] = last;
-            }
-        }
-    }
 
     // ---- join the slices
     if (C > 1) cl.sync();
     else __syncthreads();
     if (rank == 0) {
-        // the slices' sums and alternatives, each read once (the candidates' memory is free)
-        const int all = C * top_n;                                 // at most kMaxC * kTop <= LP_THREADS
-        unsigned long long k = 0;
-        if (tid < all) {
-            k = C > 1 ? cl.map_shared_rank(&sh, tid / top_n)->top[tid % top_n] : sh.top[tid];
-            sh.cand[tid] = k;
-        }
+        // the slices' sums and alternatives, each read once: slice w's list by warp w
         if (tid < C) sh.part[tid] = C > 1 ? cl.map_shared_rank(&sh, tid)->sums : sh.sums;
-        __syncthreads();
+        unsigned long long k = 0;
+        if (C > 1) {
+            if (top_n > 0) {
+                merge_block(sh.warp_top, warp < C ? cl.map_shared_rank(&sh, warp)->top[lane] : 0ull, warp, lane);
+                if (warp == 0) k = sh.warp_top[0][lane];
+            } else {
+                __syncthreads();
+            }
+        } else {
+            __syncthreads();
+            if (top_n > 0 && warp == 0) k = sh.top[lane];
+        }
         float M = -INFINITY;
         bool bad = false;
         for (int r = 0; r < C; ++r) {
@@ -501,18 +533,9 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(int V, const ch
                 logprobs[t] = (bad || target < 0 || target >= V) ? NAN : (x_target - M) - ln1;
             if (entropy != nullptr) entropy[t] = bad ? NAN : ln1 - TT * kLn2 / (1.0f + L);
         }
-        // rank the slices' alternatives among one another
-        if (k != 0) {
-            int r = tid;
-            if (C > 1) {
-                r = 0;
-                for (int j = 0; j < all; ++j) r += sh.cand[j] > k;
-            }
-            if (r < top_n) {
-                const int id = pair_id(k);
-                top_ids[static_cast<long long>(t) * top_n + r] = id;
-                top_lp[static_cast<long long>(t) * top_n + r] = bad ? NAN : (key_value(static_cast<uint32_t>(k >> 32)) - M) - ln1;
-            }
+        if (warp == 0 && lane < top_n && k != 0) {
+            top_ids[static_cast<long long>(t) * top_n + lane] = pair_id(k);
+            top_lp[static_cast<long long>(t) * top_n + lane] = bad ? NAN : (key_value(static_cast<uint32_t>(k >> 32)) - M) - ln1;
         }
     }
     if (C > 1) cl.sync();                                          // rank 0 has read the others' memory
