@@ -146,22 +146,34 @@ struct Shares {
 
 struct ScanShared {
     long long warp_sum[32];
-    long long rem;
+    long long rem, per;                  // of the sequence that was looked for: units in front, units of a head
+    SeqInfo s;
     int b;
 };
 
-// All units of the call; called by every thread of the block. *before: units in front of
-// this thread's sequences [*b0, *b1).
-__device__ __forceinline__ long long scan_units(const AttnArgs& a, Tiling g, ScanShared& sh, long long* before, int* b0,
-                                                int* b1) {
-    const int per = (a.c.B + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
-    *b0 = min(a.c.B, static_cast<int>(threadIdx.x) * per);
-    *b1 = min(a.c.B, *b0 + per);
+// A thread's part of the scan: its sequences [b0, b1), the units in front of them, and the
+// first one's lengths
+struct ScanThread {
+    long long before, per;
+    int b0, b1;
+    SeqInfo s;
+};
+
+// All units of the call; called by every thread of the block.
+__device__ __forceinline__ long long scan_units(const AttnArgs& a, Tiling g, ScanShared& sh, ScanThread& me) {
+    const int each = (a.c.B + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
+    me.b0 = min(a.c.B, static_cast<int>(threadIdx.x) * each);
+    me.b1 = min(a.c.B, me.b0 + each);
     long long mine = 0;
-    for (int b = *b0; b < *b1; ++b) {
+    for (int b = me.b0; b < me.b1; ++b) {
         const SeqInfo s = seq_info(a.c, b, a.T, attn_max_new(a));
         if (!s.ok && blockIdx.x == 0) report(a.status, MOE_ERR_DEVICE, b);
-        mine += head_units(a, s, g) * a.c.n_kv;
+        const long long per = head_units(a, s, g);
+        if (b == me.b0) {
+            me.s = s;
+            me.per = per;
+        }
+        mine += per * a.c.n_kv;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     long long inc = mine;
@@ -177,7 +189,7 @@ __device__ __forceinline__ long long scan_units(const AttnArgs& a, Tiling g, Sca
         if (w < warp) base += sh.warp_sum[w];
         W += sh.warp_sum[w];
     }
-    *before = base + inc - mine;
+    me.before = base + inc - mine;
     return W;
 }
 
@@ -219,25 +231,31 @@ struct Cursor {
 };
 
 // The place of unit x (0 <= x < W), by every thread of the block, after scan_units.
-__device__ __forceinline__ Cursor seek(const AttnArgs& a, Tiling g, ScanShared& sh, long long x, long long before, int b0,
-                                       int b1) {
-    if (x >= before) {
-        long long rem = x - before;
-        for (int b = b0; b < b1; ++b) {
-            const long long n = head_units(a, seq_info(a.c, b, a.T, attn_max_new(a)), g) * a.c.n_kv;
-            if (rem < n) {
+__device__ __forceinline__ Cursor seek(const AttnArgs& a, Tiling g, ScanShared& sh, long long x, const ScanThread& me) {
+    if (x >= me.before) {
+        long long rem = x - me.before;
+        SeqInfo s = me.s;
+        long long per = me.per;
+        for (int b = me.b0; b < me.b1; ++b) {
+            if (b > me.b0) {
+                s = seq_info(a.c, b, a.T, attn_max_new(a));
+                per = head_units(a, s, g);
+            }
+            if (rem < per * a.c.n_kv) {
                 sh.b = b;
+                sh.s = s;
                 sh.rem = rem;
+                sh.per = per;
                 break;
             }
-            rem -= n;
+            rem -= per * a.c.n_kv;
         }
     }
     __syncthreads();
     Cursor c;
     c.b = sh.b;
-    c.s = seq_info(a.c, c.b, a.T, attn_max_new(a));
-    const long long per = head_units(a, c.s, g);
+    c.s = sh.s;
+    const long long per = sh.per;
     c.h = static_cast<int>(div_pos(sh.rem, per));
     long long rem = sh.rem - c.h * per;
     c.mt = 0;
@@ -313,31 +331,42 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, const Partials& p, i
                                          int r, int rr, int lane) {
     auto slot = [&](int i) { return 2 * static_cast<size_t>(first + i) + (i == 0); };
     float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(p.ml + (slot(i) * M + r) * 2));
+    float2 own = make_float2(-INFINITY, 0.f);                      // lane i: part i's (of the first 32)
+    for (int i = lane; i < parts; i += 32) {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ml + (slot(i) * M + r) * 2));
+        if (i < 32) own = v;
+        m = fmaxf(m, v.x);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     const float ref = m == -INFINITY ? 0.f : m;
     float l = 0.f, acc[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) acc[j] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-        const size_t at = slot(i) * M + r;
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ml + at * 2));
-        const float f = exp2f(v.x - ref);
-        float o[EPL];
-        if constexpr (EPL == 2) {
-            *reinterpret_cast<float2*>(o) = __ldcg(reinterpret_cast<const float2*>(p.o + at * 64) + lane);
-        } else {
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+        if (p0 > 0) own = p0 + lane < parts ? __ldcg(reinterpret_cast<const float2*>(p.ml + (slot(p0 + lane) * M + r) * 2)) : make_float2(-INFINITY, 0.f);
+        const float f = exp2f(own.x - ref);
+        l += own.y * f;
+        const int n = min(32, parts - p0);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const size_t at = slot(p0 + i) * M + r;
+            const float w = __shfl_sync(0xFFFFFFFFu, f, i);
+            float o[EPL];
+            if constexpr (EPL == 2) {
+                *reinterpret_cast<float2*>(o) = __ldcg(reinterpret_cast<const float2*>(p.o + at * 64) + lane);
+            } else {
 #pragma unroll
-            for (int q = 0; q < EPL / 4; ++q)
-                *reinterpret_cast<float4*>(o + 4 * q) =
-                    __ldcg(reinterpret_cast<const float4*>(p.o + at * (32 * EPL)) + lane * (EPL / 4) + q);
+                for (int q = 0; q < EPL / 4; ++q)
+                    *reinterpret_cast<float4*>(o + 4 * q) =
+                        __ldcg(reinterpret_cast<const float4*>(p.o + at * (32 * EPL)) + lane * (EPL / 4) + q);
+            }
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) acc[j] += o[j] * w;
         }
-        l += v.y * f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) acc[j] += o[j] * f;
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
     const int i = token_of(a, rr), head = h * a.group + rr - i * a.group;
     const long long row = row0 + i;
     const float inv = l == 0.f ? 0.f : a.c.v_scale / l;

@@ -137,13 +137,12 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
         ptx::prefetch_tmap(&p.tk);
         ptx::prefetch_tmap(&p.tv);
     }
-    long long before;
-    int b0, b1;
-    const long long W = scan_units(a, G, scan, &before, &b0, &b1);         // (synchronises)
+    ScanThread me;
+    const long long W = scan_units(a, G, scan, me);         // (synchronises)
     const Shares shares(W, gridDim.x, 1 + S::EXTRA);
     if (static_cast<int>(blockIdx.x) >= shares.count) return;
     const long long x0 = shares.begin(blockIdx.x), x1 = shares.begin(blockIdx.x + 1);
-    Cursor cur = seek(a, G, scan, x0, before, b0, b1);
+    Cursor cur = seek(a, G, scan, x0, me);
     long long left = x1 - x0;
     int lo, hi;
     if (!cur.segment(a, G, left, lo, hi)) return;
@@ -639,16 +638,16 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
         if (!whole) {
             // the last block to leave its part of the item joins them
             const int2 in = item_shares(shares, cur, G, x1, left);
-            __threadfence();
             compute_sync();
             if (threadIdx.x == 0) {
+                __threadfence();                                   // (the barrier put the others' writes before it)
                 const bool last = atomicAdd(p.part.arrived + in.x, 1u) == static_cast<unsigned>(in.y) - 1u;
                 if (last) p.part.arrived[in.x] = 0;
                 s_last = last;
+                __threadfence();
             }
             compute_sync();
             if (s_last) {
-                __threadfence();
                 for (int r = warp; r < M && cur.mt * M + r < rows; r += NW)
                     join_row<EPL>(a, p.part, M, in.x, in.y, s.row0, cur.h, r, cur.mt * M + r, lane);
             }

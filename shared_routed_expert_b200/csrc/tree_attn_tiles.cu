@@ -164,14 +164,13 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
         ptx::prefetch_tmap(&p.tk);
         ptx::prefetch_tmap(&p.tv);
     }
-    long long before;
-    int b0, b1;
-    const long long W = scan_units(a, G, scan, &before, &b0, &b1);
+    ScanThread me;
+    const long long W = scan_units(a, G, scan, me);
     const Shares shares(W, gridDim.x, 4 + kTileExtra);
     if (threadIdx.x == 0) p.part.items[blockIdx.x].parts = 0;
     if (static_cast<int>(blockIdx.x) >= shares.count) return;
     const long long x0 = shares.begin(blockIdx.x), x1 = shares.begin(blockIdx.x + 1);
-    Cursor cur = seek(a, G, scan, x0, before, b0, b1);
+    Cursor cur = seek(a, G, scan, x0, me);
     long long left = x1 - x0;
     int lo, hi;
     if (warp == 8) {
