@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
     unsigned char* mem = ring + wk * NG * 2 * S::KBYTES;           // this group's ring: K, V, K, V, ...
     const uint32_t mem_u = ptx::smem_u32(mem);
     const bool flip = a.scale_log2 < 0.f;                          // a negative scale: q changes sign instead
-    const float scale = fabsf(a.scale_log2);
+    const float scale = fmaxf(fabsf(a.scale_log2), 1.0e-37f);      // (0 would turn what is not seen into NaN)
     // key k's row begins at k * ROWB of a span, its 16-byte chunk c lies at c ^ f(k)
     auto swz = [](int key) { return S::ROWB == 128 ? (key & 7) << 4 : ((key >> 1) & 3) << 4; };
     // where this lane's rows of the matrix loads begin in K and V, and the swizzle of their columns
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                         for (int j = 0; j < 4; ++j)
                             *reinterpret_cast<uint32_t*>(dst + (j >> 1) * 32 + (j & 1) * 16) =
                                 pack_f16x2(__uint_as_float(w[j] << 16) * d, __uint_as_float(w[j] & 0xFFFF0000u) * d);
-                        if (ch == 0) q_scale[r] = scale * exp2_int(e);
+                        if (ch == 0) q_scale[r] = fmaxf(scale * exp2_int(e), 1.0e-37f);
                     }
                 }
             }
@@ -372,14 +372,7 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                             mma16816<true>(sacc[n], q1, e4m3x2_to_f16x2(w1[n]), e4m3x2_to_f16x2(w1[n] >> 16));
                     }
                 }
-                // ---- scores in base 2, what a row does not see at -infinity
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    sacc[n][0] *= sc0;
-                    sacc[n][1] *= sc0;
-                    sacc[n][2] *= sc1;
-                    sacc[n][3] *= sc1;
-                }
+                // ---- what a row does not see at -infinity
                 if (vm != ALL || c0 + CK > s.ctx) {
                     const uint32_t see0 = seen_bits(a, s, i0, c0, keys) & vm, see1 = seen_bits(a, s, i1, c0, keys) & vm;
 #pragma unroll
@@ -411,11 +404,12 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                     pages_of(ch, k + NG);
                     load(ch, done + NG, false);
                 }
-                const bool up0 = x0m > m0 + 8.f || (m0 == -INFINITY && x0m > m0);
-                const bool up1 = x1m > m1 + 8.f || (m1 == -INFINITY && x1m > m1);
+                // (m0, m1: unscaled)
+                const bool up0 = (x0m - m0) * sc0 > 8.f || (m0 == -INFINITY && x0m > m0);
+                const bool up1 = (x1m - m1) * sc1 > 8.f || (m1 == -INFINITY && x1m > m1);
                 if (__any_sync(0xFFFFFFFFu, up0 || up1)) {
                     const float n0 = up0 ? x0m : m0, n1 = up1 ? x1m : m1;
-                    const float f0 = up0 ? ex2(m0 - n0) : 1.f, f1 = up1 ? ex2(m1 - n1) : 1.f;
+                    const float f0 = up0 ? ex2((m0 - n0) * sc0) : 1.f, f1 = up1 ? ex2((m1 - n1) * sc1) : 1.f;
                     m0 = n0;
                     m1 = n1;
                     l0 *= f0;
@@ -428,13 +422,13 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                         o[n][3] *= f1;
                     }
                 }
-                const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
+                const float ref0 = m0 == -INFINITY ? 0.f : m0 * sc0, ref1 = m1 == -INFINITY ? 0.f : m1 * sc1;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    sacc[n][0] = ex2(sacc[n][0] - ref0);
-                    sacc[n][1] = ex2(sacc[n][1] - ref0);
-                    sacc[n][2] = ex2(sacc[n][2] - ref1);
-                    sacc[n][3] = ex2(sacc[n][3] - ref1);
+                    sacc[n][0] = ex2(fmaf(sacc[n][0], sc0, -ref0));
+                    sacc[n][1] = ex2(fmaf(sacc[n][1], sc0, -ref0));
+                    sacc[n][2] = ex2(fmaf(sacc[n][2], sc1, -ref1));
+                    sacc[n][3] = ex2(fmaf(sacc[n][3], sc1, -ref1));
                     l0 += sacc[n][0] + sacc[n][1];
                     l1 += sacc[n][2] + sacc[n][3];
                 }
@@ -514,7 +508,9 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
             if (leads) begin(nch);
         }
 
-        // ---- the warps' results meet in shared memory
+        // ---- the warps' results meet in shared memory, maxima in base 2
+        m0 *= sc0;
+        m1 *= sc1;
 #pragma unroll
         for (int off = 1; off < 4; off <<= 1) {
             l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, off);
