@@ -71,4 +71,13 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
     return lo | (hi << 16);
 }
 
+// four E4M3 codes -> four fp16 (exact)
+__device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t v) {
+    uint2 r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(r.x), "=r"(r.y)
+        : "r"(v));
+    return r;
+}
+
 }  // namespace sre

@@ -45,7 +45,7 @@ struct Small {
     static constexpr int RING = D == 256 ? 131072 : 65536;
     static constexpr int NG = RING / (WK * 2 * KBYTES) < 4 ? RING / (WK * 2 * KBYTES) : 4;   // chunks a group holds
     static_assert(NG >= 1, "a group's ring holds a chunk");
-    static constexpr int EXTRA = WM == 4 ? 2 : 1;                  // what an item costs besides its steps, in steps
+    static constexpr int EXTRA = 2;                  // what an item costs besides its steps, in steps
     static constexpr int PITCH = D + 8;                            // floats per row of the merge buffer
     static constexpr int BUF = WK / 2 * M * PITCH * 4;             // half of the groups' results
     static constexpr int QPITCH = D * 2 + 16;                      // bytes per row of Q, which lies there before
@@ -84,12 +84,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// two E4M3 codes (16 bits) -> two fp16
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
-    return r;
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -365,12 +359,25 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                                          : "memory");
                         }
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            mma16816<true>(sacc[n], q0, e4m3x2_to_f16x2(w0[n]), e4m3x2_to_f16x2(w0[n] >> 16));
+                        for (int n = 0; n < NT; ++n) {
+                            const uint2 c = e4m3x4_to_f16x4(w0[n]);
+                            mma16816<true>(sacc[n], q0, c.x, c.y);
+                        }
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            mma16816<true>(sacc[n], q1, e4m3x2_to_f16x2(w1[n]), e4m3x2_to_f16x2(w1[n] >> 16));
+                        for (int n = 0; n < NT; ++n) {
+                            const uint2 c = e4m3x4_to_f16x4(w1[n]);
+                            mma16816<true>(sacc[n], q1, c.x, c.y);
+                        }
                     }
+                }
+                // K has been read: the next one
+                __syncwarp();
+                if constexpr (WM > 1) {
+                    if (lane == 0) ptx::mbar_arrive(&kfree[wk][stage]);
+                }
+                if (leads && k + NG < ch.n) {
+                    pages_of(ch, k + NG);
+                    load(ch, done + NG, false);
                 }
                 // ---- what a row does not see at -infinity
                 if (vm != ALL || c0 + CK > s.ctx) {
@@ -394,15 +401,6 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                 for (int off = 1; off < 4; off <<= 1) {
                     x0m = fmaxf(x0m, __shfl_xor_sync(0xFFFFFFFFu, x0m, off));
                     x1m = fmaxf(x1m, __shfl_xor_sync(0xFFFFFFFFu, x1m, off));
-                }
-                // K has been read: the next one
-                if constexpr (WM > 1) {
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&kfree[wk][stage]);
-                }
-                if (leads && k + NG < ch.n) {
-                    pages_of(ch, k + NG);
-                    load(ch, done + NG, false);
                 }
                 // (m0, m1: unscaled)
                 const bool up0 = (x0m - m0) * sc0 > 8.f || (m0 == -INFINITY && x0m > m0);
@@ -476,9 +474,10 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                             }
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const uint32_t u = __byte_perm(r[2 * e], 0, 0x3120), v = __byte_perm(r[2 * e + 1], 0, 0x3120);
-                                mma16816<true>(o[4 * blk + 2 * e], pf, e4m3x2_to_f16x2(u), e4m3x2_to_f16x2(v));
-                                mma16816<true>(o[4 * blk + 2 * e + 1], pf, e4m3x2_to_f16x2(u >> 16), e4m3x2_to_f16x2(v >> 16));
+                                const uint2 u = e4m3x4_to_f16x4(__byte_perm(r[2 * e], 0, 0x3120));
+                                const uint2 v = e4m3x4_to_f16x4(__byte_perm(r[2 * e + 1], 0, 0x3120));
+                                mma16816<true>(o[4 * blk + 2 * e], pf, u.x, v.x);
+                                mma16816<true>(o[4 * blk + 2 * e + 1], pf, u.y, v.y);
                             }
                         }
                     }

@@ -29,7 +29,7 @@ namespace {
 
 constexpr int TK = 128;                  // keys per step
 constexpr int TL_THREADS = 320, TL_THREADS_F8 = 384;
-constexpr int kTileExtra = 2;            // what an item costs besides its steps, in steps
+constexpr int kTileExtra = 4;            // what an item costs besides its steps, in steps
 // Rows of a kv head from which this kernel takes over. Above 32 rows each 16 of them cost the
 // other kernel (tree_attn_small.cu) a pass over K and V in shared memory: 32 sequences of 4 rows
 // of 96 heads (48 rows a kv head), 566 MB of bf16 cache: 138 us here, 195 us there.
@@ -74,13 +74,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-// two E4M3 codes (the low 16 bits) -> two fp16
-__device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t v) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
     return r;
 }
 
@@ -403,8 +396,8 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                         uint4 v = *reinterpret_cast<const uint4*>(src + key * S::ROWB + ((ch ^ swz) << 4));
                         // keys that are not there count as zero, not as whatever lies there
                         if (!(info[step_no % kInfo][key >> 5] >> (key & 31) & 1)) v = make_uint4(0, 0, 0, 0);
-                        const uint4 lo16 = make_uint4(f16_of_e4m3(v.x), f16_of_e4m3(v.x >> 16), f16_of_e4m3(v.y), f16_of_e4m3(v.y >> 16));
-                        const uint4 hi16 = make_uint4(f16_of_e4m3(v.z), f16_of_e4m3(v.z >> 16), f16_of_e4m3(v.w), f16_of_e4m3(v.w >> 16));
+                        const uint2 c0 = e4m3x4_to_f16x4(v.x), c1 = e4m3x4_to_f16x4(v.y), c2 = e4m3x4_to_f16x4(v.z), c3 = e4m3x4_to_f16x4(v.w);
+                        const uint4 lo16 = make_uint4(c0.x, c0.y, c1.x, c1.y), hi16 = make_uint4(c2.x, c2.y, c3.x, c3.y);
                         // dimensions 16 ch .. of the key: two chunks of span ch / 4; the spans' lanes take them
                         // in opposite order, for the banks
                         unsigned char* at = dst + (ch >> 2) * S::SPAN + key * 128;
@@ -443,7 +436,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                     constexpr int LPR = D / 8, RPI = 32 / LPR;
                     unsigned char* dst = smem + h * S::QHALF;
                     const int ch = lane % LPR;                     // 16-byte chunk of the row
-                    constexpr int BATCH = 8;                       // loads in flight together, before the stores
+                    constexpr int BATCH = 32 / RPI;                // all loads in flight together, before the stores
 #pragma unroll 1
                     for (int k0 = 0; k0 < 32 / RPI; k0 += BATCH) {
                         uint4 in[BATCH];
