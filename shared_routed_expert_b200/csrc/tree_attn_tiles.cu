@@ -374,8 +374,14 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
         }
     } else if (F8 && warp >= 10) {
         // ------------------------------------------------------------ E4M3 codes to fp16
-        constexpr int CPR = D / 16;                                // 16-byte chunks of codes per key
-        const int tid = threadIdx.x - 320;
+        // a thread has one 16-byte chunk of codes of every KPI-th key (8 or 16: the swizzles stay the same)
+        constexpr int CPR = D / 16, KPI = 64 / CPR;
+        const int tid = threadIdx.x - 320, key0 = tid / CPR, ch = tid % CPR;
+        const int from = key0 * S::ROWB + ((ch ^ (S::ROWB == 128 ? key0 & 7 : (key0 >> 1) & 3)) << 4);
+        // its 16 dimensions are two chunks of span ch / 4, which the spans' lanes write in opposite
+        // order, for the banks
+        const bool swap = (ch >> 2) & 1;
+        const int to = (ch >> 2) * S::SPAN + key0 * 128, to_first = ((2 * (ch & 3) + swap) ^ (key0 & 7)) << 4;
         uint32_t n = 0, step_no = 0;
         bool ok = true;
         while (ok && cur.segment(a, G, left, lo, hi)) {
@@ -387,23 +393,19 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                          ptx::mbar_wait(&empty[sl], ((n / NS) & 1u) ^ 1u, abort_flag, p.wait_limit, a.status, 11u);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
-                    const unsigned char* src = codes + rw * S::CODES;
-                    unsigned char* dst = ring + sl * S::SLOT;
-#pragma unroll 4
-                    for (int c = tid; c < TK * CPR; c += 64) {
-                        const int key = c / CPR, ch = c % CPR;
-                        const int swz = S::ROWB == 128 ? key & 7 : (key >> 1) & 3;
-                        uint4 v = *reinterpret_cast<const uint4*>(src + key * S::ROWB + ((ch ^ swz) << 4));
+                    const uint32_t* word = info[step_no % kInfo];
+                    const bool partial = (word[0] & word[1] & word[2] & word[3]) != 0xFFFFFFFFu;
+                    const unsigned char* src = codes + rw * S::CODES + from;
+                    unsigned char* dst = ring + sl * S::SLOT + to;
+#pragma unroll 8
+                    for (int i = 0; i < TK / KPI; ++i) {
+                        uint4 v = *reinterpret_cast<const uint4*>(src + i * KPI * S::ROWB);
                         // keys that are not there count as zero, not as whatever lies there
-                        if (!(info[step_no % kInfo][key >> 5] >> (key & 31) & 1)) v = make_uint4(0, 0, 0, 0);
+                        if (partial && !(word[(key0 + i * KPI) >> 5] >> ((key0 + i * KPI) & 31) & 1)) v = make_uint4(0, 0, 0, 0);
                         const uint2 c0 = e4m3x4_to_f16x4(v.x), c1 = e4m3x4_to_f16x4(v.y), c2 = e4m3x4_to_f16x4(v.z), c3 = e4m3x4_to_f16x4(v.w);
                         const uint4 lo16 = make_uint4(c0.x, c0.y, c1.x, c1.y), hi16 = make_uint4(c2.x, c2.y, c3.x, c3.y);
-                        // dimensions 16 ch .. of the key: two chunks of span ch / 4; the spans' lanes take them
-                        // in opposite order, for the banks
-                        unsigned char* at = dst + (ch >> 2) * S::SPAN + key * 128;
-                        const int first = 2 * (ch & 3) + ((ch >> 2) & 1), second = first ^ 1;
-                        *reinterpret_cast<uint4*>(at + ((first ^ (key & 7)) << 4)) = (first & 1) ? hi16 : lo16;
-                        *reinterpret_cast<uint4*>(at + ((second ^ (key & 7)) << 4)) = (second & 1) ? hi16 : lo16;
+                        *reinterpret_cast<uint4*>(dst + i * KPI * 128 + to_first) = swap ? hi16 : lo16;
+                        *reinterpret_cast<uint4*>(dst + i * KPI * 128 + (to_first ^ 16)) = swap ? lo16 : hi16;
                     }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
@@ -437,12 +439,11 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                     unsigned char* dst = smem + h * S::QHALF;
                     const int ch = lane % LPR;                     // 16-byte chunk of the row
                     constexpr int BATCH = 32 / RPI;                // all loads in flight together, before the stores
-#pragma unroll 1
-                    for (int k0 = 0; k0 < 32 / RPI; k0 += BATCH) {
+                    {
                         uint4 in[BATCH];
 #pragma unroll
                         for (int k = 0; k < BATCH; ++k) {
-                            const int r = sub * 32 + (k0 + k) * RPI + lane / LPR;
+                            const int r = sub * 32 + k * RPI + lane / LPR;
                             in[k] = make_uint4(0, 0, 0, 0);
                             if (r < rows) {
                                 const int rr = r_first + r, i = token_of(a, rr);
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                         }
 #pragma unroll
                         for (int k = 0; k < BATCH; ++k) {
-                            const int r = sub * 32 + (k0 + k) * RPI + lane / LPR;
+                            const int r = sub * 32 + k * RPI + lane / LPR;
                             uint4 v = make_uint4(in[k].x ^ sign, in[k].y ^ sign, in[k].z ^ sign, in[k].w ^ sign);
                             if constexpr (F8) {
                                 // the row's largest finite entry, over the D / 8 lanes that hold it
