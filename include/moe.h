@@ -298,6 +298,13 @@ void moe_inject_fold_timeout(int n_calls);
  * is involved. */
 void moe_inject_route_timeout(int n_calls);
 
+/* Failure-injection hook for moe_tree_attention: the next n_calls calls run with
+ * loads that are never issued and a wait limit of about 10 ms; the waits run
+ * out, the kernels drain, free TMEM and return, and MOE_ERR_TIMEOUT is left in
+ * the workspace's status word (the outputs of those calls are garbage, and the
+ * workspace has to be zeroed before the next call). No GPU fault is involved. */
+void moe_inject_attention_timeout(int n_calls);
+
 /* Fused QK-norm + partial RoPE on the attention's q and k heads, in place.
  * "GLM4-MoE生产环境优化：SGLang降低65%首Token延迟", section 2.2 QK-Norm-RoPE
  * fusion, and the de/en pages, section 2 "Qknorm Fusion": both steps are
@@ -418,12 +425,15 @@ moe_status moe_qk_norm_rope_append(const moe_kv_cache* cache, const moe_kv_batch
  * A row that sees nothing (or only scores of -infinity) gives zeros and -infinity.
  * Keys and values that a row does not see do not reach it, whatever they hold.
  *   q    [T] rows of n_q * head_dim bf16, q_stride elements apart
- *   out  the same with out_stride; lse [T][n_q]
- *   ws   moe_tree_attention_workspace_size bytes, 256-byte aligned, zeroed once
- *        by the caller before the first use; bad contents of the batch's arrays
- *        leave MOE_ERR_DEVICE in its status word (moe_get_status): the rows of a
- *        sequence with bad lengths are left as they were, a block of keys with a
- *        bad page id counts as not seen
+ *   out  the same with out_stride (may be q itself with the same stride); lse
+ *        [T][n_q]
+ *   ws   moe_tree_attention_workspace_size bytes, 256-byte aligned, zeroed by the
+ *        caller before the first use (and after a MOE_ERR_TIMEOUT) and kept for
+ *        this entry point, which finds its counters in it as the last call left
+ *        them; bad contents of the batch's arrays leave MOE_ERR_DEVICE in its
+ *        status word (moe_get_status): the rows of a sequence with bad lengths
+ *        are left as they were, a block of keys with a bad page id counts as not
+ *        seen
  * n_q a multiple of n_kv, n_q <= 1024; row strides multiples of 8; softmax_scale
  * finite. The result does not depend on the timing of the run (no atomics in the
  * sums), but a row's rounding may depend on the other sequences of the batch. */

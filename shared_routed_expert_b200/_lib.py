@@ -25,7 +25,8 @@ EXPORTS = ("moe_workspace_size", "moe_route_topk", "moe_permute", "moe_grouped_f
            "moe_profile_reset", "moe_profile_read", "moe_inject_wait_timeout",
            "moe_permute_noalloc", "moe_qk_norm_rope", "moe_cast_f32_bf16", "moe_inject_fold_timeout",
            "moe_inject_route_timeout", "moe_qk_norm_rope_append", "moe_tree_attention",
-           "moe_tree_attention_workspace_size", "moe_kv_compact", "moe_token_logprobs")
+           "moe_tree_attention_workspace_size", "moe_kv_compact", "moe_token_logprobs",
+           "moe_inject_attention_timeout")
 
 
 class MoeError(RuntimeError):
@@ -103,6 +104,8 @@ def lib() -> C.CDLL:
         L.moe_cast_f32_bf16.argtypes = [sz, p, p, p]
         L.moe_qk_norm_rope.restype = i
         L.moe_qk_norm_rope.argtypes = [i, i, i, i, i, f, p, p, i, p, p, p, p, p]
+        L.moe_inject_attention_timeout.restype = None
+        L.moe_inject_attention_timeout.argtypes = [i]
         i64, KC, KB = C.c_int64, C.POINTER(moe_kv_cache), C.POINTER(moe_kv_batch)
         L.moe_qk_norm_rope_append.restype = i
         L.moe_qk_norm_rope_append.argtypes = [KC, KB, i, i, i, f, p, i64, p, i, p, p, p, p, i64, p, p]
@@ -227,10 +230,12 @@ def moe_quant_rows_e4m3(rows, cols, inp, codes, scales, stream=None):
 # (the checks are written for speed: a decoding step calls these once per layer, and a
 # launch is shorter than a few dozen attribute look-ups)
 
-def _rows(name, t, dtype):
-    """Row stride of a tensor whose rows are dense: [T, n] or [T, heads, d]."""
+def _rows(name, t, dtype, device):
+    """Row stride and row length of a tensor whose rows are dense: [T, n] or [T, heads, d]."""
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}")
     stride, shape = t.stride(), t.shape
     inner = 1
     for i in range(len(shape) - 1, 0, -1):
@@ -240,10 +245,12 @@ def _rows(name, t, dtype):
     return (stride[0] if shape[0] > 1 else max(inner, stride[0])), inner
 
 
-def _dense(name, t, dtype, shape):
-    """Address of a contiguous tensor of that type and shape (None: any shape)."""
+def _dense(name, t, dtype, shape, device):
+    """Address of a contiguous tensor of that type and shape (None: any shape) on that device."""
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} has to be contiguous")
     if shape is not None and t.shape != shape:
@@ -251,24 +258,26 @@ def _dense(name, t, dtype, shape):
     return t.data_ptr()
 
 
-def _launch(name, fn, t, stream, *args):
-    """Calls an entry point on `stream` (None: the current one) with t's device current."""
-    at = t.device.index
-    if at is None or at == _current_device():
-        rc = fn(*args, _raw_stream(at) if stream is None and at is not None else _stream(stream))
+def _launch(name, fn, device, stream, *args):
+    """Calls an entry point on `stream` (None: the device's current one) with the tensors'
+    device current."""
+    if device < 0:
+        raise ValueError(f"{name}: the tensors have to be on a CUDA device")
+    if device == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(at):
+        with torch.cuda.device(device):
             rc = fn(*args, _stream(stream))
     if rc != MOE_OK:
         raise MoeError(name, rc)
 
 
-def _current_device():
-    return torch.cuda.current_device()
-
-
-def _raw_stream(device):
-    return torch._C._cuda_getCurrentRawStream(device)
+def _device_of(t, cache, batch):
+    """The device index that a call's tensor, cache and batch share."""
+    device = t.get_device()
+    if cache.device != device or batch.device != device:
+        raise ValueError(f"the cache and the batch have to be on {t.device}, where the rows are")
+    return device
 
 
 def make_kv_cache(k, v, k_scale: float = 1.0, v_scale: float = 1.0) -> moe_kv_cache:
@@ -284,7 +293,7 @@ def make_kv_cache(k, v, k_scale: float = 1.0, v_scale: float = 1.0) -> moe_kv_ca
         raise TypeError(f"a cache of {k.dtype}")
     c = moe_kv_cache(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), k.shape[0], k.shape[2],
                      k.shape[1], k.shape[3], dt, k_scale, v_scale)
-    c.tensors = (k, v)
+    c.tensors, c.device = (k, v), k.get_device()
     return c
 
 
@@ -292,11 +301,10 @@ def make_kv_batch(q_start, ctx_len, page_table, max_new: int) -> moe_kv_batch:
     """moe_kv_batch of int32 device tensors q_start [B + 1], ctx_len [B], page_table
     [B, max_pages]; it keeps them alive, and calls read what they hold at the time."""
     B = ctx_len.shape[0]
-    _dense("q_start", q_start, torch.int32, (B + 1,))
-    _dense("ctx_len", ctx_len, torch.int32, (B,))
-    _dense("page_table", page_table, torch.int32, (B, page_table.shape[1]))
-    b = moe_kv_batch(q_start.data_ptr(), ctx_len.data_ptr(), page_table.data_ptr(), B, page_table.shape[1], max_new)
-    b.tensors = (q_start, ctx_len, page_table)
+    i32, device = torch.int32, ctx_len.get_device()
+    b = moe_kv_batch(_dense("q_start", q_start, i32, (B + 1,), device), _dense("ctx_len", ctx_len, i32, (B,), device),
+                     _dense("page_table", page_table, i32, (B, page_table.shape[1]), device), B, page_table.shape[1], max_new)
+    b.tensors, b.device = (q_start, ctx_len, page_table), device
     return b
 
 
@@ -304,22 +312,22 @@ def moe_qk_norm_rope_append(cache, batch, n_q: int, rot: int, eps: float, qkv, p
                             q_out, bad_tokens=None, stream=None):
     """qkv [T, (n_q + 2 n_kv) d] bf16 -> q_out [T, n_q d] bf16 and the cache (see
     include/moe.h); q_norm_w / k_norm_w None: no norm, rot 0: no rotation."""
-    d, T = cache.head_dim, qkv.shape[0]
+    d, T, dev = cache.head_dim, qkv.shape[0], _device_of(qkv, cache, batch)
     bf16 = torch.bfloat16
-    qs, qn = _rows("qkv", qkv, bf16)
-    os_, on = _rows("q_out", q_out, bf16)
+    qs, qn = _rows("qkv", qkv, bf16, dev)
+    os_, on = _rows("q_out", q_out, bf16, dev)
     width = (n_q + 2 * cache.n_kv) * d
     if qn != width or q_out.shape[0] != T or (on != n_q * d and on != width):
         raise ValueError("qkv [T, (n_q + 2 n_kv) d] and q_out [T, n_q d]")
-    qw = None if q_norm_w is None else _dense("q_norm_w", q_norm_w, bf16, (d,))
-    kw = None if k_norm_w is None else _dense("k_norm_w", k_norm_w, bf16, (d,))
-    bad = None if bad_tokens is None else _dense("bad_tokens", bad_tokens, torch.int32, None)
+    qw = None if q_norm_w is None else _dense("q_norm_w", q_norm_w, bf16, (d,), dev)
+    kw = None if k_norm_w is None else _dense("k_norm_w", k_norm_w, bf16, (d,), dev)
+    bad = None if bad_tokens is None else _dense("bad_tokens", bad_tokens, torch.int32, None, dev)
     max_pos, pos, cs = 0, None, None
     if rot > 0:
         max_pos = cos_sin.shape[0]
-        pos = _dense("positions", positions, torch.int32, (T,))
-        cs = _dense("cos_sin", cos_sin, torch.float32, (max_pos, rot))
-    _launch("moe_qk_norm_rope_append", lib().moe_qk_norm_rope_append, qkv, stream, cache, batch, T, n_q, rot, eps,
+        pos = _dense("positions", positions, torch.int32, (T,), dev)
+        cs = _dense("cos_sin", cos_sin, torch.float32, (max_pos, rot), dev)
+    _launch("moe_qk_norm_rope_append", lib().moe_qk_norm_rope_append, dev, stream, cache, batch, T, n_q, rot, eps,
             qkv.data_ptr(), qs, pos, max_pos, qw, kw, cs, q_out.data_ptr(), os_, bad)
 
 
@@ -343,51 +351,51 @@ def moe_tree_attention(cache, batch, n_q: int, q, out, ws, tree_mask=None, lse=N
     """q [T, n_q d] bf16 over the cache -> out [T, n_q d] bf16, lse [T, n_q] fp32 or None;
     tree_mask [T, words] int64 (bit j: the row sees its sequence's new token j) or None
     for a chain; scale None: 1 / sqrt(head dim)."""
-    T, d = q.shape[0], cache.head_dim
-    qs, qn = _rows("q", q, torch.bfloat16)
-    os_, on = _rows("out", out, torch.bfloat16)
+    T, d, dev = q.shape[0], cache.head_dim, _device_of(q, cache, batch)
+    qs, qn = _rows("q", q, torch.bfloat16, dev)
+    os_, on = _rows("out", out, torch.bfloat16, dev)
     if out.shape[0] != T or qn != n_q * d or on != qn:
         raise ValueError("q and out: [T, n_q d]")
-    ls = None if lse is None else _dense("lse", lse, torch.float32, (T, n_q))
+    ls = None if lse is None else _dense("lse", lse, torch.float32, (T, n_q), dev)
     words, mask = 0, None
     if tree_mask is not None:
         words = tree_mask.shape[1]
-        mask = _dense("tree_mask", tree_mask, torch.int64, (T, words))
-    _launch("moe_tree_attention", lib().moe_tree_attention, q, stream, cache, batch, T, n_q,
-            d ** -0.5 if scale is None else scale, q.data_ptr(), qs, mask, words, out.data_ptr(), os_, ls, ws.data_ptr(),
-            ws.numel())
+        mask = _dense("tree_mask", tree_mask, torch.int64, (T, words), dev)
+    wp = _dense("ws", ws, torch.uint8, None, dev)
+    _launch("moe_tree_attention", lib().moe_tree_attention, dev, stream, cache, batch, T, n_q,
+            d ** -0.5 if scale is None else scale, q.data_ptr(), qs, mask, words, out.data_ptr(), os_, ls, wp, ws.numel())
 
 
 def moe_kv_compact(cache, batch, accepted, n_accepted, n_layers: int = 1, layer_stride: int = 0, bad_seqs=None,
                    stream=None):
     """Moves accepted [B, max_accept] int32 new tokens' keys and values to the front of
     their sequences' new tokens, in place, in n_layers caches layer_stride elements apart."""
-    B, most = batch.B, accepted.shape[1]
-    acc = _dense("accepted", accepted, torch.int32, (B, most))
-    n = _dense("n_accepted", n_accepted, torch.int32, (B,))
-    bad = None if bad_seqs is None else _dense("bad_seqs", bad_seqs, torch.int32, None)
-    _launch("moe_kv_compact", lib().moe_kv_compact, accepted, stream, cache, batch, n_layers, layer_stride, acc, most, n, bad)
+    B, most, dev = batch.B, accepted.shape[1], _device_of(accepted, cache, batch)
+    acc = _dense("accepted", accepted, torch.int32, (B, most), dev)
+    n = _dense("n_accepted", n_accepted, torch.int32, (B,), dev)
+    bad = None if bad_seqs is None else _dense("bad_seqs", bad_seqs, torch.int32, None, dev)
+    _launch("moe_kv_compact", lib().moe_kv_compact, dev, stream, cache, batch, n_layers, layer_stride, acc, most, n, bad)
 
 
 def moe_token_logprobs(logits, targets, logprobs, entropy=None, top_ids=None, top_logprobs=None, stream=None):
     """logits [T, V] (bf16 or fp32, dense rows) and targets [T] int32 -> logprobs [T],
     entropy [T], top_ids / top_logprobs [T, n], each fp32 (ids int32) or None."""
     T, V = logits.shape
-    dt = logits.dtype
+    dt, dev = logits.dtype, logits.get_device()
     code = MOE_BF16 if dt == torch.bfloat16 else MOE_F32 if dt == torch.float32 else None
     if code is None:
         raise TypeError(f"logits are {dt}, not bf16 or fp32")
     f32 = torch.float32
-    tg = None if targets is None else _dense("targets", targets, torch.int32, (T,))
-    lp = None if logprobs is None else _dense("logprobs", logprobs, f32, (T,))
-    en = None if entropy is None else _dense("entropy", entropy, f32, (T,))
+    tg = None if targets is None else _dense("targets", targets, torch.int32, (T,), dev)
+    lp = None if logprobs is None else _dense("logprobs", logprobs, f32, (T,), dev)
+    en = None if entropy is None else _dense("entropy", entropy, f32, (T,), dev)
     n = 0 if top_ids is None else top_ids.shape[1]
     ids = top = None
     if n:
-        ids = _dense("top_ids", top_ids, torch.int32, (T, n))
-        top = _dense("top_logprobs", top_logprobs, f32, (T, n))
-    _launch("moe_token_logprobs", lib().moe_token_logprobs, logits, stream, T, V, code, logits.data_ptr(),
-            _rows("logits", logits, dt)[0], tg, n, lp, en, ids, top)
+        ids = _dense("top_ids", top_ids, torch.int32, (T, n), dev)
+        top = _dense("top_logprobs", top_logprobs, f32, (T, n), dev)
+    _launch("moe_token_logprobs", lib().moe_token_logprobs, dev, stream, T, V, code, logits.data_ptr(),
+            _rows("logits", logits, dt, dev)[0], tg, n, lp, en, ids, top)
 
 
 def moe_get_status(ws, stream=None) -> int:
@@ -430,6 +438,10 @@ def moe_inject_fold_timeout(n_calls: int):
 
 def moe_inject_route_timeout(n_calls: int):
     lib().moe_inject_route_timeout(int(n_calls))
+
+
+def moe_inject_attention_timeout(n_calls: int):
+    lib().moe_inject_attention_timeout(int(n_calls))
 
 
 def moe_profile_read(name: str):

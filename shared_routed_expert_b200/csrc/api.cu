@@ -545,7 +545,7 @@ const char* moe_status_string(moe_status s) {
         case MOE_ERR_WORKSPACE: return "workspace too small";
         case MOE_ERR_CUDA: return "CUDA error";
         case MOE_ERR_TIMEOUT: return "device wait timed out";
-        case MOE_ERR_DEVICE: return "bad data on device (expert id out of range)";
+        case MOE_ERR_DEVICE: return "bad data on device (expert or page id or length out of range)";
     }
     return "unknown status";
 }

@@ -64,8 +64,8 @@ struct AppendArgs {
     int32_t* bad;
 };
 
-// LPH lanes per head; SH: half of rot modulo 8 (where a dimension's rotation partner lies among
-// a lane's 8); KI: instructions' worth of heads per warp.
+// LPH lanes per head; SH: half of rot modulo 8 (how far a dimension's rotation partner lies from it
+// among a lane's 8); KI: instructions' worth of heads per warp.
 template <int LPH, int SH, int KI, bool F8>
 __global__ void __launch_bounds__(AP_WARPS * 32, 4) append_kernel(const AppendArgs a, const KvView c) {
     constexpr int D = 8 * LPH, HPI = 32 / LPH, HPW = KI * HPI;
@@ -128,8 +128,7 @@ __global__ void __launch_bounds__(AP_WARPS * 32, 4) append_kernel(const AppendAr
     uint4 wq = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u), wk = wq;   // 1.0
     if (a.q_w != nullptr && h0 < a.n_q) wq = reinterpret_cast<const uint4*>(a.q_w)[L];
     if (a.k_w != nullptr && h0 + nh > a.n_q) wk = reinterpret_cast<const uint4*>(a.k_w)[L];
-    // dimension d's partner is d + half in the first half and d - half in the second: element
-    // (j + SH) % 8 of the lane that holds it
+    // dimension d's partner is d + half in the first half and d - half in the second
     int src[NP];
     bool turns[NP];
 #pragma unroll
@@ -160,8 +159,14 @@ __global__ void __launch_bounds__(AP_WARPS * 32, 4) append_kernel(const AppendAr
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = v[j] * r * w[j];
     };
-    // every lane offers its element (j + SH) % 8 and takes its partner's
-    auto partner = [&](const float (&u)[8], int j) { return __shfl_sync(0xFFFFFFFFu, u[(j + SH) & 7], src[j / PS]); };
+    // every lane offers the element its taker is after: (j + SH) % 8 to a taker in the first half of the
+    // rotating dimensions, (j - SH) % 8 to one in the second
+    auto partner = [&](const float (&u)[8], int j) {
+        const float o = __shfl_sync(0xFFFFFFFFu, u[(j + SH) & 7], src[j / PS]);
+        if constexpr (SH % 4 == 0) return o;
+        const float p2 = __shfl_sync(0xFFFFFFFFu, u[(j - SH) & 7], src[j / PS]);
+        return i0 + j < half ? o : p2;
+    };
 
     if (h0 + HPW <= a.n_q && a.q_w != nullptr) {
         // q heads alone (most warps): nothing to tell apart

@@ -145,6 +145,7 @@ moe_status moe_tree_attention(const moe_kv_cache* cache, const moe_kv_batch* bat
         return MOE_ERR_INVALID_ARG;
     const int64_t width = static_cast<int64_t>(n_q) * cache->head_dim;
     if (!row_ok(q_stride, width) || !row_ok(out_stride, width)) return MOE_ERR_INVALID_ARG;
+    if (q == out && q_stride != out_stride) return MOE_ERR_INVALID_ARG;
     if (tree_mask == nullptr ? mask_words != 0 : (mask_words < 1 || (reinterpret_cast<uintptr_t>(tree_mask) & 7u)))
         return MOE_ERR_INVALID_ARG;
     if (mask_words > 64) return MOE_ERR_UNSUPPORTED;
@@ -179,6 +180,8 @@ moe_status moe_tree_attention(const moe_kv_cache* cache, const moe_kv_batch* bat
     return from_cuda(tree_attn_tiles_apply(a) ? launch_tree_attn_tiles(a, partials, st)
                                               : launch_tree_attn_small(a, partials, st));
 }
+
+void moe_inject_attention_timeout(int n_calls) { tree_attn_inject_stall(n_calls > 0 ? n_calls : 0); }
 
 moe_status moe_kv_compact(const moe_kv_cache* cache, const moe_kv_batch* batch, int32_t n_layers,
                           int64_t layer_stride, const int32_t* accepted, int32_t max_accept,

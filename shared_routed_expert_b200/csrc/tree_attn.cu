@@ -3,6 +3,8 @@
 //   s_j = softmax_scale * q . k_j over the keys a row sees, m = max s, p_j = e^{s_j - m},
 //   out = sum p_j v_j / sum p_j,  lse = m + ln sum p_j.
 // Here: the join of partial results, and the cache's TMA maps.
+#include <atomic>
+
 #include "kernels.cuh"
 #include "tree_attn.cuh"
 
@@ -11,6 +13,7 @@ namespace sre {
 namespace {
 
 constexpr int JN_WARPS = 4;
+std::atomic<int> g_stall{0};
 
 // Joins the items that a cut between two shares goes through: block x the one that begins
 // in share x and does not end there; a warp per row. Bound by latency (a few hundred KB out
@@ -41,6 +44,15 @@ EncodeTiledFn encode_tiled() {
 }
 
 }  // namespace
+
+void tree_attn_inject_stall(int n_calls) { g_stall.store(n_calls); }
+
+bool tree_attn_take_stall() {
+    int n = g_stall.load();
+    while (n > 0)
+        if (g_stall.compare_exchange_weak(n, n - 1)) return true;
+    return false;
+}
 
 // K or V of a cache as (dimension within a 128-byte span, slot, span, kv head, page): a box
 // is one span of box_rows slots of one head, stored [slot][128 bytes] (64 for 64-byte

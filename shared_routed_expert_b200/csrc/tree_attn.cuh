@@ -391,6 +391,9 @@ cudaError_t launch_tree_attn_join(const AttnArgs& a, int M, Partials p, int bloc
 Partials partials_at(void* mem, int blocks, int M);
 size_t partials_bytes(int blocks, int M, int head_dim);
 bool make_kv_map(CUtensorMap* m, const AttnArgs& a, bool v, int box_rows);
+// testing hook: the next n calls run with loads that are never issued and a ~10 ms wait limit
+void tree_attn_inject_stall(int n_calls);
+bool tree_attn_take_stall();
 bool tree_attn_tiles_apply(const AttnArgs& a);
 cudaError_t launch_tree_attn_tiles(const AttnArgs& a, void* partials, cudaStream_t st);
 

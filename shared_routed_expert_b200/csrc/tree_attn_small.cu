@@ -60,6 +60,7 @@ struct SmallParams {
     Partials part;
     int box_shift;                       // log2 of the rows of a TMA box
     long long wait_limit;
+    bool stall;                          // testing: no loads
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
     // K (or V) of the chunk that pages_of looked at, the group's count-th; its stage has been read
     // once WM warps have freed it
     auto load = [&](const Chunks& k, uint32_t count, bool is_v) {
-        if (lane == 0) {
+        if (lane == 0 && !p.stall) {
             const uint32_t st = count % NG;
             bool ok = true;
             if (WM > 1 && count >= NG)
@@ -677,7 +678,8 @@ cudaError_t launch_cfg(const AttnArgs& a, void* partials, int sms, cudaStream_t 
     const int page = 1 << a.c.page_shift;
     const int box = page < S::CK ? page : S::CK;
     p.box_shift = page < S::CK ? a.c.page_shift : (S::CK == 32 ? 5 : 4);
-    p.wait_limit = 4ll << 30;
+    p.stall = tree_attn_take_stall();
+    p.wait_limit = p.stall ? 20ll << 20 : 4ll << 30;
     if (!make_kv_map(&p.tk, a, false, box) || !make_kv_map(&p.tv, a, true, box)) return cudaErrorInvalidValue;
     const int blocks = sms * S::BLOCKS_PER_SM < kSmallBlocks ? sms * S::BLOCKS_PER_SM : kSmallBlocks;
     p.part = partials_at(partials, blocks, S::M);

@@ -57,6 +57,7 @@ struct TileParams {
     Partials part;
     int box_shift;
     long long wait_limit;
+    bool stall;                          // testing: no loads
 };
 
 // pairs of fp32 in one register pair: one instruction for two multiply-adds or additions
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
         // ------------------------------------------------------------ producer
         const int box = 1 << p.box_shift, pieces = TK >> p.box_shift;
         uint32_t n = 0, step_no = 0, tail_phase = 0;               // slots and steps so far
-        bool ok = true;
+        bool ok = !p.stall;
         while (ok && cur.segment(a, G, left, lo, hi)) {
             const int keys = tile_keys(a, cur.s, cur.mt, G.M);
             const int32_t* table = a.c.page_table + static_cast<size_t>(cur.b) * a.c.max_pages;
@@ -713,7 +714,8 @@ cudaError_t launch_tiles(const AttnArgs& a, void* partials, int sms, cudaStream_
     const int page = 1 << a.c.page_shift;
     const int box = page < TK ? page : TK;
     p.box_shift = page < TK ? a.c.page_shift : 7;
-    p.wait_limit = 16ll << 30;
+    p.stall = tree_attn_take_stall();
+    p.wait_limit = p.stall ? 20ll << 20 : 16ll << 30;
     if (!make_kv_map(&p.tk, a, false, box) || !make_kv_map(&p.tv, a, true, box)) return cudaErrorInvalidValue;
     const int blocks = sms < kTileBlocks ? sms : kTileBlocks;
     p.part = partials_at(partials, blocks, kTileRows);

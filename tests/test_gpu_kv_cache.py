@@ -38,6 +38,14 @@ APPEND = [
     ([40, 1], [3, 255], 6, 3, 64, 0, 128, "hnd"),
     ([300], [11], 12, 1, 128, 64, 256, "nhd"),
     ([1] * 70, list(range(70)), 3, 3, 128, 64, 16, "hnd"),
+    # rotations whose halves end inside a lane's dimensions
+    ([9, 4], [2, 30], 5, 1, 128, 24, 16, "hnd"),
+    ([9, 4], [2, 30], 5, 1, 64, 36, 16, "hnd"),
+    ([9, 4], [2, 30], 4, 2, 64, 8, 16, "nhd"),
+    ([9, 4], [2, 30], 4, 4, 64, 12, 16, "hnd"),
+    ([700], [100], 24, 2, 128, 64, 64, "hnd"),              # more heads than the SMs hold at once
+    ([600, 13], [3, 90], 13, 13, 64, 32, 16, "hnd"),
+    ([400], [0], 30, 10, 256, 256, 32, "hnd"),
 ]
 
 

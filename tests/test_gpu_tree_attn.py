@@ -70,6 +70,10 @@ SHAPES = [
     ([257, 19], [0, 513], 24, 2, 128, 64, "hnd"),
     ([300], [77], 2, 1, 256, 32, "interleaved"),
     ([700, 1, 40], [1111, 900, 0], 16, 2, 128, 128, "hnd"),
+    ([1, 2, 1], [700, 0, 255], 12, 1, 128, 256, "hnd"),    # pages longer than a chunk of keys
+    ([3], [100], 12, 1, 64, 16, "hnd"),                    # 36 rows: both halves of a tile on the same rows
+    ([10, 11, 22], [5, 64, 200], 12, 1, 128, 32, "hnd"),   # 120, 132 and 264 rows
+    ([2, 1], [4000, 130], 1024, 16, 64, 64, "hnd"),        # 64 query heads to a kv head
 ]
 
 
@@ -340,3 +344,66 @@ def test_other_stream_and_two_workspaces_at_once():
     torch.cuda.synchronize()
     for ws, out, lse in res:
         check(P, q, n_q, out, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n_of", [lambda b: (b * 7) % 3, lambda b: 1 + (b * 5) % 40])
+def test_more_sequences_than_threads(n_of, kv):
+    """700 sequences (several to a thread of the kernels' scan), empty ones among them."""
+    n = [n_of(b) for b in range(700)]
+    ctx = [(b * 37) % 90 for b in range(700)]
+    P = Paged(n, ctx, 1, 64, 16, kv, seed=21, rows=sum(n) + 1)
+    q = make_q(P, 2)
+    out, lse, st = run(P, q, 2)
+    assert st == _lib.MOE_OK
+    check(P, q, 2, out, lse)
+
+
+def test_one_workspace_serves_every_kind_of_call():
+    """Decoding, drafts and chunks in turn on one workspace, at several head widths."""
+    ws = None
+    for rounds in range(2):
+        for n, ctx, n_q, n_kv, d, kv in (([1, 1], [3000, 50], 12, 1, 128, "bf16"), ([40, 3], [700, 0], 12, 1, 128, "e4m3"),
+                                         ([2], [5000], 8, 1, 256, "bf16"), ([1], [900], 8, 2, 64, "e4m3"),
+                                         ([300], [600], 12, 1, 128, "bf16"), ([30], [2000], 4, 2, 256, "e4m3")):
+            P = Paged(n, ctx, n_kv, d, 64, kv, seed=22 + rounds)
+            cache, batch = P.handles(m)
+            if ws is None:
+                wide = Paged([1], [1], 1, 256, 16, "bf16").handles(m)[0]
+                ws = m.alloc_tree_attention_workspace(wide, 4, 512)
+            q = make_q(P, n_q)
+            out, lse = torch.full_like(q, 7.5), torch.full((P.T, n_q), 7.5, device=DEV)
+            m.moe_tree_attention(cache, batch, n_q, q, out, ws, lse=lse)
+            assert m.moe_get_status(ws) == _lib.MOE_OK
+            check(P, q, n_q, out, lse)
+
+
+@pytest.mark.parametrize("n,ctx", [([1] * 5, [3000] * 5), ([50, 9], [1500, 70])])
+def test_output_over_the_queries(n, ctx):
+    P = Paged(n, ctx, 1, 128, 64, "bf16", seed=24)
+    q = make_q(P, 12)
+    out, lse, _ = run(P, q, 12)
+    q2 = q.clone()
+    cache, batch = P.handles(m)
+    ws = m.alloc_tree_attention_workspace(cache, 12, P.T)
+    m.moe_tree_attention(cache, batch, 12, q2, q2, ws)
+    assert torch.equal(q2.view(torch.int16), out.view(torch.int16))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,d", [(1, 128), (3, 256), (30, 128), (5, 64)])
+def test_waits_that_run_out_are_reported(n, d, kv):
+    """Loads that never come: the bounded waits run out, the kernels return and say so, and a
+    zeroed workspace works again."""
+    P = Paged([n, n], [900, 40], 1, d, 16, kv, seed=25)
+    q = make_q(P, 12)
+    cache, batch = P.handles(m)
+    ws = m.alloc_tree_attention_workspace(cache, 12, P.T)
+    out, lse = torch.empty_like(q), torch.empty(P.T, 12, device=DEV)
+    _lib.moe_inject_attention_timeout(1)
+    m.moe_tree_attention(cache, batch, 12, q, out, ws, lse=lse)
+    assert m.moe_get_status(ws) == _lib.MOE_ERR_TIMEOUT
+    ws.zero_()
+    m.moe_tree_attention(cache, batch, 12, q, out, ws, lse=lse)
+    assert m.moe_get_status(ws) == _lib.MOE_OK
+    check(P, q, 12, out, lse)

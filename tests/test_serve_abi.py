@@ -103,7 +103,7 @@ def test_attention_refusals(L):
                      (dict(scale=float("inf")), BAD), (dict(scale=float("nan")), BAD), (dict(q=None), BAD), (dict(q=FAKE + 2), BAD),
                      (dict(qs=511), BAD), (dict(qs=508), BAD), (dict(out=None), BAD), (dict(os=516), BAD), (dict(lse=FAKE + 2), BAD),
                      (dict(ws=None), BAD), (dict(ws=FAKE + 16), BAD), (dict(n=10), WS), (dict(words=1), BAD),
-                     (dict(mask=FAKE), BAD), (dict(mask=FAKE + 4, words=1), BAD), (dict(mask=FAKE, words=65), UNSUP)]:
+                     (dict(out=FAKE, os=520), BAD), (dict(mask=FAKE), BAD), (dict(mask=FAKE + 4, words=1), BAD), (dict(mask=FAKE, words=65), UNSUP)]:
         assert attend(L, **kw) == want, kw
     assert attend(L, mask=FAKE, words=1, b=batch(max_new=65)) == BAD
     for b in (batch(B=0), batch(max_new=0)):
@@ -157,3 +157,44 @@ def test_python_binding_refuses_tensors_that_do_not_fit():
         m.moe_token_logprobs(torch.zeros(2, 8), i32(3), torch.zeros(2))
     with pytest.raises(ValueError):
         m.moe_qk_norm_rope_append(c, b, 4, 64, 1e-5, q, i32(4), None, None, torch.zeros(10, 64), q)
+
+
+def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
+    """Tensors of another device than the current one: it is made current for the launch; tensors of
+    the CPU, or of several devices, are refused."""
+    seen = []
+
+    class on:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            seen.append(("enter", self.d))
+
+        def __exit__(self, *exc):
+            seen.append(("exit", self.d))
+
+    class stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: stream)
+    _lib._launch("f", lambda *a: seen.append(a) or 0, 1, None, 5)
+    assert seen == [("enter", 1), (5, 77), ("exit", 1)]
+    with pytest.raises(_lib.MoeError):
+        _lib._launch("f", lambda *a: 2, 1, stream, 5)
+    with pytest.raises(ValueError):
+        _lib._launch("f", lambda *a: 0, -1, None)
+    k = torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16)
+    c = m.make_kv_cache(k, k.clone())
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    b = m.make_kv_batch(i32(3), i32(2), i32(2, 4), 5)
+    q = torch.zeros(4, 4 * 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):                          # everything on the CPU
+        m.moe_tree_attention(c, b, 4, q, torch.empty_like(q), torch.zeros(1 << 10, dtype=torch.uint8))
+    c.device = 0
+    with pytest.raises(ValueError):                          # the cache elsewhere
+        m.moe_tree_attention(c, b, 4, q, torch.empty_like(q), torch.zeros(1 << 10, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        m.moe_token_logprobs(torch.zeros(2, 8), i32(2), torch.zeros(2))
