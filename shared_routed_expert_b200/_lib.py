@@ -237,6 +237,8 @@ def _rows(name, t, dtype, device):
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}")
     stride, shape = t.stride(), t.shape
+    if len(shape) == 2 and stride[1] == 1 and shape[0] > 1:
+        return stride[0], shape[1]
     inner = 1
     for i in range(len(shape) - 1, 0, -1):
         if stride[i] != inner and shape[i] != 1:
@@ -263,7 +265,7 @@ def _launch(name, fn, device, stream, *args):
     device current."""
     if device < 0:
         raise ValueError(f"{name}: the tensors have to be on a CUDA device")
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(device):

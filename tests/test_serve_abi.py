@@ -177,7 +177,7 @@ def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
     class stream:
         cuda_stream = 77
 
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch.cuda, "device", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: stream)
     _lib._launch("f", lambda *a: seen.append(a) or 0, 1, None, 5)
