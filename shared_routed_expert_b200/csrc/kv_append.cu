@@ -248,8 +248,7 @@ void append_sh(const AppendArgs& a, const KvView& c, bool f8, cudaStream_t st) {
 // front of their destinations and nobody else touches its column, so reading a few
 // tokens ahead of the writes keeps the move in place and free of barriers.
 constexpr int CP_THREADS = 256;
-constexpr int CP_AHEAD = 4;              // tokens read before the first of them is written
-constexpr int CP_COLS = 2;               // columns per thread: two loads in flight for each token ahead
+constexpr int CP_AHEAD = 8;              // tokens read before the first of them is written
 
 __global__ void __launch_bounds__(CP_THREADS) compact_kernel(const KvView c, int n_layers, long long layer_b,
                                                              const int32_t* __restrict__ accepted, int max_accept,
@@ -284,33 +283,25 @@ __global__ void __launch_bounds__(CP_THREADS) compact_kernel(const KvView c, int
         return;
     }
     const long long cols = static_cast<long long>(n_layers) * 2 * c.n_kv * row_chunks;
-    char* base[CP_COLS];
-#pragma unroll
-    for (int q = 0; q < CP_COLS; ++q) {
-        const long long col = (static_cast<long long>(blockIdx.x) * CP_COLS + q) * CP_THREADS + threadIdx.x;
-        const int chunk = static_cast<int>(col % row_chunks);
-        long long rest = col / row_chunks;
-        const int h = static_cast<int>(rest % c.n_kv);
-        rest /= c.n_kv;
-        base[q] = col < cols ? ((rest & 1) ? c.v : c.k) + (rest >> 1) * layer_b + h * c.head_b + chunk * 16 : nullptr;
-    }
+    const long long col = static_cast<long long>(blockIdx.x) * CP_THREADS + threadIdx.x;
+    if (col >= cols) return;
+    const int chunk = static_cast<int>(col % row_chunks);
+    long long rest = col / row_chunks;
+    const int h = static_cast<int>(rest % c.n_kv);
+    rest /= c.n_kv;
+    char* base = ((rest & 1) ? c.v : c.k) + (rest >> 1) * layer_b + h * c.head_b + chunk * 16;
     for (int i0 = 0; i0 < n; i0 += CP_AHEAD) {
-        uint4 x[CP_COLS][CP_AHEAD];
+        uint4 x[CP_AHEAD];
 #pragma unroll
         for (int j = 0; j < CP_AHEAD; ++j) {
             const int i = i0 + j;
-            if (i >= n || cp_off[i] == cp_off[max_accept + i]) continue;
-#pragma unroll
-            for (int q = 0; q < CP_COLS; ++q)
-                if (base[q] != nullptr) x[q][j] = *reinterpret_cast<const uint4*>(base[q] + cp_off[i]);
+            if (i < n && cp_off[i] != cp_off[max_accept + i]) x[j] = *reinterpret_cast<const uint4*>(base + cp_off[i]);
         }
 #pragma unroll
         for (int j = 0; j < CP_AHEAD; ++j) {
             const int i = i0 + j;
-            if (i >= n || cp_off[i] == cp_off[max_accept + i]) continue;
-#pragma unroll
-            for (int q = 0; q < CP_COLS; ++q)
-                if (base[q] != nullptr) *reinterpret_cast<uint4*>(base[q] + cp_off[max_accept + i]) = x[q][j];
+            if (i < n && cp_off[i] != cp_off[max_accept + i])
+                *reinterpret_cast<uint4*>(base + cp_off[max_accept + i]) = x[j];
         }
     }
 }
@@ -338,7 +329,7 @@ cudaError_t launch_compact(const KvView& c, int row_bytes, int n_layers, long lo
     ProfileScope ps("kv_compact", st);
     const int row_chunks = row_bytes / 16;
     const long long cols = static_cast<long long>(n_layers) * 2 * c.n_kv * row_chunks;
-    const dim3 grid(static_cast<unsigned>((cols + CP_THREADS * CP_COLS - 1) / (CP_THREADS * CP_COLS)), c.B);
+    const dim3 grid(static_cast<unsigned>((cols + CP_THREADS - 1) / CP_THREADS), c.B);
     compact_kernel<<<grid, CP_THREADS, 2 * sizeof(long long) * max_accept, st>>>(c, n_layers, layer_b, accepted,
                                                                                  max_accept, n_accepted, row_chunks, bad);
     note_launch();
