@@ -348,21 +348,28 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, const Partials& p, i
         const float f = exp2f(own.x - ref);
         l += own.y * f;
         const int n = min(32, parts - p0);
-#pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const size_t at = slot(p0 + i) * M + r;
-            const float w = __shfl_sync(0xFFFFFFFFu, f, i);
-            float o[EPL];
-            if constexpr (EPL == 2) {
-                *reinterpret_cast<float2*>(o) = __ldcg(reinterpret_cast<const float2*>(p.o + at * 64) + lane);
-            } else {
+        // AT_ONCE parts' loads are in flight together; behind the last part the weights are 0
+        constexpr int AT_ONCE = 4;
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += AT_ONCE) {
 #pragma unroll
-                for (int q = 0; q < EPL / 4; ++q)
-                    *reinterpret_cast<float4*>(o + 4 * q) =
-                        __ldcg(reinterpret_cast<const float4*>(p.o + at * (32 * EPL)) + lane * (EPL / 4) + q);
+            for (int e = 0; e < AT_ONCE; ++e) {
+                const size_t at = slot(p0 + min(i0 + e, n - 1)) * M + r;
+                const float w = __shfl_sync(0xFFFFFFFFu, f, i0 + e);
+                float o[EPL];
+                if constexpr (EPL == 2) {
+                    *reinterpret_cast<float2*>(o) = __ldcg(reinterpret_cast<const float2*>(p.o + at * 64) + lane);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < EPL / 4; ++q)
+                        *reinterpret_cast<float4*>(o + 4 * q) =
+                            __ldcg(reinterpret_cast<const float4*>(p.o + at * (32 * EPL)) + lane * (EPL / 4) + q);
+                }
+                if (i0 + e < n) {
+#pragma unroll
+                    for (int j = 0; j < EPL; ++j) acc[j] += o[j] * w;
+                }
             }
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) acc[j] += o[j] * w;
         }
     }
 #pragma unroll
