@@ -39,8 +39,17 @@ __device__ __forceinline__ bool sees_new(const AttnArgs& a, int t, int i, int j)
     return (a.mask[static_cast<size_t>(t) * a.mask_words + (j >> 6)] >> (j & 63)) & 1;
 }
 
+// (special-function unit: 2 ulp; what goes through it is rounded to bf16, or a sum whose logarithm is taken)
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2F = 0.6931471805599453f;
+
+// ln sum 2^s from the maximum m (base 2) and l = sum 2^(s - m); -infinity for l = 0
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2F; }
 
 // One query row over cache indexes [lo, hi), key by key, by one warp: lane l holds
 // dimensions EPL*l .. of q (scaled by scale_log2) and of acc. m, l: running maximum
@@ -345,7 +354,7 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, const Partials& p, i
     for (int j = 0; j < EPL; ++j) acc[j] = 0.f;
     for (int p0 = 0; p0 < parts; p0 += 32) {
         if (p0 > 0) own = p0 + lane < parts ? __ldcg(reinterpret_cast<const float2*>(p.ml + (slot(p0 + lane) * M + r) * 2)) : make_float2(-INFINITY, 0.f);
-        const float f = exp2f(own.x - ref);
+        const float f = fast_exp2(own.x - ref);
         l += own.y * f;
         const int n = min(32, parts - p0);
         // AT_ONCE parts' loads are in flight together; behind the last part the weights are 0
@@ -376,7 +385,7 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, const Partials& p, i
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
     const int i = token_of(a, rr), head = h * a.group + rr - i * a.group;
     const long long row = row0 + i;
-    const float inv = l == 0.f ? 0.f : a.c.v_scale / l;
+    const float inv = l == 0.f ? 0.f : __fdividef(a.c.v_scale, l);
     uint32_t w[EPL / 2];
 #pragma unroll
     for (int j = 0; j < EPL; j += 2) w[j / 2] = l == 0.f ? 0u : pack_bf16x2(acc[j] * inv, acc[j + 1] * inv);
@@ -384,7 +393,7 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, const Partials& p, i
     if constexpr (EPL == 2) *reinterpret_cast<uint32_t*>(dst) = w[0];
     else if constexpr (EPL == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[EPL / 2 - 2], w[EPL / 2 - 1]);
-    if (a.lse != nullptr && lane == 0) a.lse[row * a.n_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2F;
+    if (a.lse != nullptr && lane == 0) a.lse[row * a.n_q + head] = lse_of(m, l);
 }
 
 constexpr int kSmallBlocks = 320;        // most blocks of the 16- to 64-row kernel

@@ -86,11 +86,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // What a group loads of an item: its chunks start at key `first` and lie SK keys apart.
@@ -408,7 +403,7 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                 const bool up1 = (x1m - m1) * sc1 > 8.f || (m1 == -INFINITY && x1m > m1);
                 if (__any_sync(0xFFFFFFFFu, up0 || up1)) {
                     const float n0 = up0 ? x0m : m0, n1 = up1 ? x1m : m1;
-                    const float f0 = up0 ? ex2((m0 - n0) * sc0) : 1.f, f1 = up1 ? ex2((m1 - n1) * sc1) : 1.f;
+                    const float f0 = up0 ? fast_exp2((m0 - n0) * sc0) : 1.f, f1 = up1 ? fast_exp2((m1 - n1) * sc1) : 1.f;
                     m0 = n0;
                     m1 = n1;
                     l0 *= f0;
@@ -424,10 +419,10 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                 const float ref0 = m0 == -INFINITY ? 0.f : m0 * sc0, ref1 = m1 == -INFINITY ? 0.f : m1 * sc1;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    sacc[n][0] = ex2(fmaf(sacc[n][0], sc0, -ref0));
-                    sacc[n][1] = ex2(fmaf(sacc[n][1], sc0, -ref0));
-                    sacc[n][2] = ex2(fmaf(sacc[n][2], sc1, -ref1));
-                    sacc[n][3] = ex2(fmaf(sacc[n][3], sc1, -ref1));
+                    sacc[n][0] = fast_exp2(fmaf(sacc[n][0], sc0, -ref0));
+                    sacc[n][1] = fast_exp2(fmaf(sacc[n][1], sc0, -ref0));
+                    sacc[n][2] = fast_exp2(fmaf(sacc[n][2], sc1, -ref1));
+                    sacc[n][3] = fast_exp2(fmaf(sacc[n][3], sc1, -ref1));
                     l0 += sacc[n][0] + sacc[n][1];
                     l1 += sacc[n][2] + sacc[n][3];
                 }
@@ -533,10 +528,10 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                 const float2 a0 = *reinterpret_cast<const float2*>(ml[br]), a1 = *reinterpret_cast<const float2*>(ml[br + 8]);
                 const float n0 = fmaxf(m0, a0.x), n1 = fmaxf(m1, a1.x);
                 const float ref0 = n0 == -INFINITY ? 0.f : n0, ref1 = n1 == -INFINITY ? 0.f : n1;
-                f0 = ex2(m0 - ref0);
-                f1 = ex2(m1 - ref1);
-                g0 = ex2(a0.x - ref0);
-                g1 = ex2(a1.x - ref1);
+                f0 = fast_exp2(m0 - ref0);
+                f1 = fast_exp2(m1 - ref1);
+                g0 = fast_exp2(a0.x - ref0);
+                g1 = fast_exp2(a1.x - ref1);
                 m0 = n0;
                 m1 = n1;
                 l0 = l0 * f0 + a0.y * g0;
@@ -590,7 +585,7 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
             const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
             for (int w = 0; w < HK; ++w) {
-                const float f = ex2(ml[w * M + r][0] - ref);
+                const float f = fast_exp2(ml[w * M + r][0] - ref);
                 l += ml[w * M + r][1] * f;
 #pragma unroll
                 for (int j = 0; j < EPL; ++j) acc[j] += buf[(w * M + r) * S::PITCH + lane * EPL + j] * f;
@@ -613,7 +608,7 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                 attend_row<EPL, F8>(a, cur.b, s, i, cur.h, q, lo * S::SK, min(hi * S::SK, keys), m, l, acc, lane);
             }
             if (whole) {
-                const float inv = l == 0.f ? 0.f : a.c.v_scale / l;
+                const float inv = l == 0.f ? 0.f : __fdividef(a.c.v_scale, l);
                 uint32_t w[EPL / 2];
 #pragma unroll
                 for (int j = 0; j < EPL; j += 2)
@@ -623,7 +618,7 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                 else if constexpr (EPL == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
                 else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[EPL / 2 - 2], w[EPL / 2 - 1]);
                 if (a.lse != nullptr && lane == 0)
-                    a.lse[row * a.n_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2F;
+                    a.lse[row * a.n_q + head] = lse_of(m, l);
             } else {
                 float* dst = p.part.o + (slot * M + r) * D + lane * EPL;
 #pragma unroll

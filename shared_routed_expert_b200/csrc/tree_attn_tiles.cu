@@ -78,12 +78,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-__device__ __forceinline__ float tl_ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // A row of an item again, key by key (a rare path, kept out of the main code's registers)
 template <int D, bool F8>
 __device__ __noinline__ void redo_row(const AttnArgs& a, const Cursor& c, int i, int head, int lo, int hi, float* o, float* ml,
@@ -105,11 +99,11 @@ __device__ __noinline__ void redo_row(const AttnArgs& a, const Cursor& c, int i,
         }
     } else {
         const long long row = c.s.row0 + i;
-        const float inv = l == 0.f ? 0.f : a.c.v_scale / l;
+        const float inv = l == 0.f ? 0.f : __fdividef(a.c.v_scale, l);
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
             a.out[row * a.out_stride + head * D + lane * EPL + j] = f32_to_bf16(l == 0.f ? 0.f : acc[j] * inv);
-        if (a.lse != nullptr && lane == 0) a.lse[row * a.n_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2F;
+        if (a.lse != nullptr && lane == 0) a.lse[row * a.n_q + head] = lse_of(m, l);
     }
 }
 
@@ -540,7 +534,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                     const bool up = (mx - m) * scale > 8.f || (m == -INFINITY && mx > m);
                     if (__any_sync(0xFFFFFFFFu, up)) {
                         const float m2 = up ? mx : m;
-                        const float f = up ? tl_ex2((m - m2) * scale) : 1.f;
+                        const float f = up ? fast_exp2((m - m2) * scale) : 1.f;
                         m = m2;
                         l *= f;
                         if (st > from) {
@@ -566,8 +560,8 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                         for (int e = 0; e < 32; e += 2) {
                             float u, v;
                             unpair2(fma2(pair2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, ref2), u, v);
-                            u = tl_ex2(u);
-                            v = tl_ex2(v);
+                            u = fast_exp2(u);
+                            v = fast_exp2(v);
                             sum2[(e >> 1) & 1] = add2(sum2[(e >> 1) & 1], pair2(u, v));
                             pk[e / 2] = F8 ? pack_f16x2(u, v) : pack_bf16x2(u, v);
                         }
@@ -621,8 +615,8 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                     ptx::tc_fence_after();
                     const float2 o = x_ml[x];
                     const float both = fmaxf(m2, o.x), base = both == -INFINITY ? 0.f : both;
-                    f0 = tl_ex2(m2 - base);
-                    f1 = tl_ex2(o.x - base);
+                    f0 = fast_exp2(m2 - base);
+                    f1 = fast_exp2(o.x - base);
                     m2 = both;
                     l = l * f0 + o.y * f1;
                 }
@@ -636,7 +630,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                         JoinItem{item_shares(shares, cur, G, x1, left).y, s.row0, s.n * a.group, cur.h, cur.mt};
                 float* part_o = p.part.o + slot_row * D;
                 float* part_ml = p.part.ml + slot_row * 2;
-                const float inv = l == 0.f ? 0.f : a.c.v_scale / l;
+                const float inv = l == 0.f ? 0.f : __fdividef(a.c.v_scale, l);
                 bool nan = false;
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
@@ -678,7 +672,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                         part_ml[0] = m2;
                         part_ml[1] = l;
                     } else if (a.lse != nullptr) {
-                        a.lse[row * a.n_q + head] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * kLn2F;
+                        a.lse[row * a.n_q + head] = lse_of(m2, l);
                     }
                 }
                 // 0 * infinity or NaN: a value that the row may not see; again, key by key
