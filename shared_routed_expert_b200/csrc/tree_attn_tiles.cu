@@ -631,10 +631,8 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                 float* part_o = p.part.o + slot_row * D;
                 float* part_ml = p.part.ml + slot_row * 2;
                 const float inv = l == 0.f ? 0.f : __fdividef(a.c.v_scale, l);
-                bool nan = false;
-#pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t x[32];
+                // a row of O, 32 dimensions at a time, and whether it holds NaN
+                auto take = [&](int q, uint32_t (&x)[32]) {
                     ptx::tmem_ld_32x32b_x32(o_t + q * 32, x);
                     ptx::tmem_ld_wait(x);
                     if (share) {
@@ -645,9 +643,27 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                         for (int e = 0; e < 32; ++e)
                             x[e] = __float_as_uint(__uint_as_float(x[e]) * f0 + __uint_as_float(y[e]) * f1);
                     }
+                    bool n = false;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) nan |= __uint_as_float(x[e]) != __uint_as_float(x[e]);
-                    if (mine && whole) {
+                    for (int e = 0; e < 32; ++e) n |= __uint_as_float(x[e]) != __uint_as_float(x[e]);
+                    return n;
+                };
+                const bool unseen = hi * TK > s.ctx;               // the item has keys that some row may not see
+                bool nan = false, stays = false;
+                if (unseen && whole && a.out == a.q) {
+                    // in place: a row that is computed again below still needs its query
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t x[32];
+                        stays |= take(q, x);
+                    }
+                    stays &= l == l;
+                }
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t x[32];
+                    nan |= take(q, x);
+                    if (mine && whole && !stays) {
                         uint4* dst = reinterpret_cast<uint4*>(a.out + row * a.out_stride + head * D + q * 32);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -658,7 +674,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                                                                    __uint_as_float(x[e * 8 + 2 * j + 1]) * inv);
                             dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                    } else if (mine) {
+                    } else if (mine && !whole) {
                         uint4* dst = reinterpret_cast<uint4*>(part_o + q * 32);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) dst[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
@@ -677,7 +693,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                 }
                 // 0 * infinity or NaN: a value that the row may not see; again, key by key
                 __syncwarp();
-                uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && nan && l == l && hi * TK > s.ctx);
+                uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && nan && l == l && unseen);
                 while (again) {
                     const int src = __ffs(again) - 1;
                     again &= again - 1;

@@ -391,6 +391,28 @@ def test_output_over_the_queries(n, ctx):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,n_q,d", [(14, 1, 128), (40, 12, 128), (12, 8, 64), (40, 1, 256)])
+def test_output_over_the_queries_beside_values_without_a_number(n, n_q, d, kv):
+    """In place: rows that are computed again because a value they do not see holds NaN still find
+    their queries."""
+    P = Paged([n], [30], 1, d, 16, kv, seed=26)
+    sets = tree_sets(n, 11)
+    pg, sl = P.slots(0)
+    P.v[pg[30 + 2], 0, sl[30 + 2], d - 1] = 0x7F if kv == "e4m3" else math.nan
+    q = make_q(P, n_q)
+    mask = mask_tensor(sets, 1)
+    cache, batch = P.handles(m)
+    ws = m.alloc_tree_attention_workspace(cache, n_q, P.T)
+    got = q.clone()
+    m.moe_tree_attention(cache, batch, n_q, got, got, ws, tree_mask=mask)
+    ref, _, to, _ = attention_ref(P, q, n_q, sets)
+    clean = torch.tensor([not w >> 2 & 1 for w in sets], dtype=torch.bool, device=DEV)
+    assert bool(clean[3:].any()) and not bool(clean.all())
+    err = (got.view(P.T, n_q, d).double() - ref).abs() - to
+    assert float(err[clean].max()) <= 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("n,d", [(1, 128), (3, 256), (30, 128), (5, 64)])
 def test_waits_that_run_out_are_reported(n, d, kv):
     """Loads that never come: the bounded waits run out, the kernels return and say so, and a
