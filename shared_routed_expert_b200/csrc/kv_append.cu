@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(AP_WARPS * 32, 4) append_kernel(const AppendAr
     long long slot = -1;
     if (h0 + nh > a.n_q) {
         const SeqInfo s = seq_info(c, b, a.T, c.max_new);
-        if (s.ok) slot = slot_offset(c, b, s.ctx + (t - s.row0), 0);
+        if (s.ok && t >= s.row0) slot = slot_offset(c, b, s.ctx + (t - s.row0), 0);   // (q_start out of order: not followed)
         if (slot < 0 && counts && lane == 0 && a.bad != nullptr) atomicAdd(a.bad, 1);
     }
     // norm weights as they are stored (registers decide how many warps are in flight)

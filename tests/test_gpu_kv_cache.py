@@ -155,6 +155,36 @@ def test_append_counts_bad_tokens_and_stores_nothing_of_them():
     assert torch.equal((P.v.view(torch.int16) != v0.view(torch.int16)).permute(0, 2, 1, 3).any(-1).any(-1), want)
 
 
+def test_append_with_rows_out_of_order_stays_inside_the_cache():
+    """q_start [5, 40, 60, 7, 8]: the search lands row 30 in the sequence of rows 40..59, in front
+    of its first row; such tokens are counted and nothing of them is stored."""
+    n_q, n_kv, d, T = 2, 1, 128, 64
+    qkv = torch.randn(T, (n_q + 2 * n_kv) * d, device=DEV).to(torch.bfloat16)
+    k = torch.full((12, n_kv, 16, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    v = k.clone()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    table = torch.arange(12, **i32).reshape(4, 3)
+    batch = m.make_kv_batch(torch.tensor([5, 40, 60, 7, 8], **i32), torch.zeros(4, **i32), table, 40)
+    bad = torch.zeros(1, **i32)
+    q_out = torch.zeros(T, n_q * d, dtype=torch.bfloat16, device=DEV)
+    m.moe_qk_norm_rope_append(m.make_kv_cache(k, v), batch, n_q, 0, 1e-5, qkv, None, None, None, None, q_out, bad)
+    # the rows' sequences: the last entry of q_start that the search counts as reached
+    want_k, want_v, want_bad = torch.full_like(k, 7.0), torch.full_like(v, 7.0), 0
+    q_start = [5, 40, 60, 7, 8]
+    for t in range(T):
+        b = sum(s <= t for s in q_start[:4]) - 1
+        if b < 0 or t >= q_start[b + 1]:
+            continue
+        n, i = q_start[b + 1] - q_start[b], t - q_start[b]
+        if n < 0 or n > 40 or i < 0:
+            want_bad += 1
+            continue
+        want_k[table[b, i // 16], 0, i % 16] = qkv[t, n_q * d:(n_q + 1) * d]
+        want_v[table[b, i // 16], 0, i % 16] = qkv[t, (n_q + 1) * d:]
+    assert want_bad > 0 and int(bad) == want_bad
+    assert torch.equal(k, want_k) and torch.equal(v, want_v)
+
+
 def test_append_e4m3_saturates_and_keeps_nan():
     P = Paged([1], [0], 1, 64, 16, "e4m3", seed=4, k_scale=0.5, v_scale=0.25)
     cache, batch = P.handles(m)
