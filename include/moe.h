@@ -430,13 +430,15 @@ moe_status moe_qk_norm_rope_append(const moe_kv_cache* cache, const moe_kv_batch
  *   ws   moe_tree_attention_workspace_size bytes, 256-byte aligned, zeroed by the
  *        caller before the first use (and after a MOE_ERR_TIMEOUT) and kept for
  *        this entry point, which finds its counters in it as the last call left
- *        them; bad contents of the batch's arrays leave MOE_ERR_DEVICE in its
- *        status word (moe_get_status): the rows of a sequence with bad lengths
- *        are left as they were, a block of keys with a bad page id counts as not
- *        seen
+ *        them. One call at a time uses it (calls that may overlap, on several
+ *        streams or in graphs replayed side by side, have one each). Bad contents
+ *        of the batch's arrays leave MOE_ERR_DEVICE in its status word
+ *        (moe_get_status): the rows of a sequence with bad lengths are left as
+ *        they were, a block of keys with a bad page id counts as not seen
  * n_q a multiple of n_kv, n_q <= 1024; row strides multiples of 8; softmax_scale
- * finite. The result does not depend on the timing of the run (no atomics in the
- * sums), but a row's rounding may depend on the other sequences of the batch. */
+ * and softmax_scale * k_scale * log2(e) finite. The result does not depend on the
+ * timing of the run (no atomics in the sums), but a row's rounding may depend on
+ * the other sequences of the batch. */
 moe_status moe_tree_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, int32_t T, int32_t n_q,
                               float softmax_scale, const void* q, int64_t q_stride, const uint64_t* tree_mask,
                               int32_t mask_words, void* out, int64_t out_stride, float* lse, void* ws,

@@ -139,7 +139,8 @@ moe_status moe_tree_attention(const moe_kv_cache* cache, const moe_kv_batch* bat
     if (rc == MOE_OK) rc = check_batch(batch);
     if (rc == MOE_OK) rc = check_heads(*cache, n_q);
     if (rc != MOE_OK) return rc;
-    if (T < 0 || !std::isfinite(softmax_scale)) return MOE_ERR_INVALID_ARG;
+    const float scale_log2 = softmax_scale * cache->k_scale * kLog2E;
+    if (T < 0 || !std::isfinite(scale_log2)) return MOE_ERR_INVALID_ARG;
     if (T > kMaxT) return MOE_ERR_UNSUPPORTED;
     if (!q || !out || !ws || !at16(q) || !at16(out) || !at4(lse) || (reinterpret_cast<uintptr_t>(ws) & 255u))
         return MOE_ERR_INVALID_ARG;
@@ -166,7 +167,7 @@ moe_status moe_tree_attention(const moe_kv_cache* cache, const moe_kv_batch* bat
     }
     a.head_dim = cache->head_dim;
     a.f8 = cache->dtype == MOE_E4M3;
-    a.scale_log2 = softmax_scale * cache->k_scale * kLog2E;
+    a.scale_log2 = scale_log2;
     a.q = static_cast<const uint16_t*>(q);
     a.q_stride = q_stride;
     a.mask = tree_mask;

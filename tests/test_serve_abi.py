@@ -111,6 +111,13 @@ def test_attention_refusals(L):
     assert attend(L, T=0) == OK
 
 
+def test_a_scale_that_overflows_with_the_keys_scale_is_refused(L):
+    f8 = dict(dtype=_lib.MOE_E4M3, k_scale=1e30)
+    assert attend(L, c=cache(**f8), b=batch(B=0), scale=1e8) == OK       # 1.4e38
+    assert attend(L, c=cache(**f8), b=batch(B=0), scale=1e9) == BAD
+    assert attend(L, b=batch(B=0), scale=3e38) == BAD                    # ... with log2 e
+
+
 def test_compact_refusals(L):
     for kw, want in [(dict(layers=0), BAD), (dict(layers=5000), UNSUP), (dict(layers=2, ls=100), BAD), (dict(layers=2, ls=132), BAD),
                      (dict(acc=None), BAD), (dict(n=None), BAD), (dict(most=0), BAD), (dict(most=1025), UNSUP)]:
