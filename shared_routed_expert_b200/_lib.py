@@ -296,6 +296,9 @@ def make_kv_cache(k, v, k_scale: float = 1.0, v_scale: float = 1.0) -> moe_kv_ca
     c = moe_kv_cache(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), k.shape[0], k.shape[2],
                      k.shape[1], k.shape[3], dt, k_scale, v_scale)
     c.tensors, c.device = (k, v), k.get_device()
+    # elements from a view's first to behind its last one, and to the end of its allocation
+    c.extent = 1 + sum((n - 1) * s for n, s in zip(k.shape, k.stride())) if k.numel() else 0
+    c.room = min(t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() for t in (k, v))
     return c
 
 
@@ -371,8 +374,11 @@ def moe_tree_attention(cache, batch, n_q: int, q, out, ws, tree_mask=None, lse=N
 def moe_kv_compact(cache, batch, accepted, n_accepted, n_layers: int = 1, layer_stride: int = 0, bad_seqs=None,
                    stream=None):
     """Moves accepted [B, max_accept] int32 new tokens' keys and values to the front of
-    their sequences' new tokens, in place, in n_layers caches layer_stride elements apart."""
+    their sequences' new tokens, in place, in n_layers caches layer_stride elements apart
+    (the cache is the first one, all layers lie in its tensors' allocations)."""
     B, most, dev = batch.B, accepted.shape[1], _device_of(accepted, cache, batch)
+    if n_layers > 1 and (n_layers - 1) * layer_stride + cache.extent > cache.room:
+        raise ValueError("the layers reach behind the cache's allocation")
     acc = _dense("accepted", accepted, torch.int32, (B, most), dev)
     n = _dense("n_accepted", n_accepted, torch.int32, (B,), dev)
     bad = None if bad_seqs is None else _dense("bad_seqs", bad_seqs, torch.int32, None, dev)

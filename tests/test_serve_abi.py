@@ -166,6 +166,21 @@ def test_python_binding_refuses_tensors_that_do_not_fit():
         m.moe_qk_norm_rope_append(c, b, 4, 64, 1e-5, q, i32(4), None, None, torch.zeros(10, 64), q)
 
 
+def test_layers_behind_the_allocation_are_refused():
+    layers = torch.zeros(3, 4, 2, 16, 128, dtype=torch.bfloat16)
+    more = torch.zeros(3, 4, 2, 16, 128, dtype=torch.bfloat16)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    b = m.make_kv_batch(i32(3), i32(2), i32(2, 4), 5)
+    one = layers[0].numel()
+    for first, n, fits in ((0, 3, True), (0, 4, False), (1, 2, True), (1, 3, False)):
+        c = m.make_kv_cache(layers[first], more[first])
+        with pytest.raises(ValueError, match="CUDA device" if fits else "behind"):
+            m.moe_kv_compact(c, b, i32(2, 4), i32(2), n_layers=n, layer_stride=one)
+    c = m.make_kv_cache(layers[0], more[0].clone())          # V's layers are not there
+    with pytest.raises(ValueError, match="behind"):
+        m.moe_kv_compact(c, b, i32(2, 4), i32(2), n_layers=2, layer_stride=one)
+
+
 def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
     """Tensors of another device than the current one: it is made current for the launch; tensors of
     the CPU, or of several devices, are refused."""
