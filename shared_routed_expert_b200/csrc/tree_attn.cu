@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(JN_WARPS * 32) join_kernel(const AttnArgs a, c
     const JoinItem c = p.items[blockIdx.x];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int r = blockIdx.y * JN_WARPS + warp; c.parts > 0 && r < M && c.mt * M + r < c.rows; r += gridDim.y * JN_WARPS)
-        join_row<EPL>(a, p, M, blockIdx.x, c.parts, c.row0, c.h, r, c.mt * M + r, lane);
+        join_row<EPL, 4>(a, p, M, blockIdx.x, c.parts, c.row0, c.h, r, c.mt * M + r, lane);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

@@ -334,8 +334,9 @@ struct Partials {
 };
 
 // Row r of a tile of M rows (rr of the item's packed rows) from its parts in `parts` shares
-// from `first` on, by one warp: with m = max m_p, sum_p 2^{m_p - m} (l_p, o_p).
-template <int EPL>
+// from `first` on, by one warp: with m = max m_p, sum_p 2^{m_p - m} (l_p, o_p); the loads of
+// AT_ONCE parts are in flight together.
+template <int EPL, int AT_ONCE>
 __device__ __forceinline__ void join_row(const AttnArgs& a, const Partials& p, int M, int first, int parts, int row0, int h,
                                          int r, int rr, int lane) {
     auto slot = [&](int i) { return 2 * static_cast<size_t>(first + i) + (i == 0); };
@@ -357,8 +358,7 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, const Partials& p, i
         const float f = fast_exp2(own.x - ref);
         l += own.y * f;
         const int n = min(32, parts - p0);
-        // AT_ONCE parts' loads are in flight together; behind the last part the weights are 0
-        constexpr int AT_ONCE = 4;
+        // (behind the last part the weights are 0)
 #pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += AT_ONCE) {
 #pragma unroll
