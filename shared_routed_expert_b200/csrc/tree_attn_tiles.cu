@@ -15,8 +15,15 @@
 // Roles: warps 0-3 and 4-7 the two halves' softmax, loads of Q and epilogue; warp 8 issues
 // the products; warp 9 streams K and V boxes (one per page piece and 128-byte span) through
 // a ring in shared memory. Every wait is bounded.
+// Measured, 96 heads of 128 over 8 kv heads, bf16: a chunk of 4096 rows behind 12288 keys 2.77 ms,
+// 1040 TFLOP/s at the power limit of 1000 W (1.75 GHz); trees of 23 to 61 nodes of 12 sequences
+// 187 us (730 TFLOP/s; the join is 13 us of it); 4-token chains of 32 sequences 107 us, 5.3 TB/s.
+// The exponentials of a half take about as long as its products (128 per thread and step). No
+// faster for the chunk: the whole row of S in registers (2987 us, spills), a quartic in place of
+// 1/8 to 3/8 of the exponentials (3004 to 3137 us), P in two arrivals (2909 us, one 2913 then),
+// steps of 64 keys with two S (4950 us: a product of N = 64 takes as long as one of 128).
 // E4M3 caches: the boxes go to a ring of codes, from which warps 10 and 11 write K and V as
-// fp16 (exact) to the products' ring. Q rows are scaled by a power of two to fp16 (exact for
+// fp16 (exact) to the products' ring (2048 rows behind 8192 keys: 1088 us, bf16 910 us). Q rows are scaled by a power of two to fp16 (exact for
 // everything within 2^-28 of the row's largest entry) and P is fp16. (E4M3 operands would
 // need P in 4 significant bits.)
 #include "kernels.cuh"
@@ -29,10 +36,10 @@ namespace {
 
 constexpr int TK = 128;                  // keys per step
 constexpr int TL_THREADS = 320, TL_THREADS_F8 = 384;
-constexpr int kTileExtra = 4;            // what an item costs besides its steps, in steps
+constexpr int kTileExtra = 4;            // what an item costs besides its steps, in steps (2: those chains 138 us)
 // Rows of a kv head from which this kernel takes over. Above 32 rows each 16 of them cost the
 // other kernel (tree_attn_small.cu) a pass over K and V in shared memory: 32 sequences of 4 rows
-// of 96 heads (48 rows a kv head), 566 MB of bf16 cache: 138 us here, 195 us there.
+// of 96 heads (48 rows a kv head), 566 MB of bf16 cache: 107 us here, 195 us there.
 constexpr int kTileLeastRows = 32;
 constexpr int kInfo = 8;                 // steps whose key masks are kept (the producer is at most 6 ahead)
 
@@ -340,8 +347,8 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                     const bool more = st + 1 < hi;
                     const uint32_t vn = n + 1, kn = n + 2;
                     if (!wait(&full[vn % NS], (vn / NS) & 1u, 3u)) break;
-    #pragma unroll 1
-                for (int h = 0; h < (two ? 2 : 1); ++h) {
+#pragma unroll 1
+                    for (int h = 0; h < (two ? 2 : 1); ++h) {
                         if (!wait(&p_ready[h], pp[h], 5u)) break;
                         pp[h] ^= 1u;
                         ptx::tc_fence_after();
