@@ -45,7 +45,7 @@ typedef enum moe_status {
     MOE_ERR_WORKSPACE = 3,     /* ws_bytes smaller than moe_workspace_size() */
     MOE_ERR_CUDA = 4,          /* a CUDA runtime/driver call failed */
     MOE_ERR_TIMEOUT = 5,       /* a kernel's bounded wait ran out (device-side) */
-    MOE_ERR_DEVICE = 6         /* bad data seen on the device (e.g. expert id out of range) */
+    MOE_ERR_DEVICE = 6         /* bad data seen on the device (e.g. expert or page id out of range) */
 } moe_status;
 
 typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2 } moe_dtype;

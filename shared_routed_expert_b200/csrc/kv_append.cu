@@ -9,9 +9,9 @@
 // lanes hold 8 dimensions each (16-byte loads and stores) and a warp's instruction covers 1, 2
 // or 4 heads of 256, 128 or 64 dimensions. The sums of squares are added in the order of
 // qknorm.cu's 32 lanes (partial sums of head_dim / 32 dimensions, a butterfly over them), and
-// the products are formed alike, so q rows and bf16 keys have the same bits. (4 dimensions a
-// lane and a head per instruction: 104 instructions a head, 86 us for 5 prompts of 5949 tokens,
-// 96 + 8 + 8 heads of 128.)
+// the products are formed alike, so q rows and bf16 keys have the same bits. 5 prompts of 5949
+// tokens, 96 + 8 + 8 heads of 128, 340 MB: 78 us, 4.4 TB/s; the warps wait on their loads and
+// butterflies (4 dimensions a lane and a head per instruction: 104 instructions a head, 86 us).
 #include "kernels.cuh"
 #include "kv_cache.cuh"
 
@@ -246,7 +246,9 @@ void append_sh(const AppendArgs& a, const KvView& c, bool f8, cudaStream_t st) {
 // Compaction. A thread owns one 16-byte column of one (layer, K or V, head) of a
 // sequence and walks the accepted tokens in ascending order: sources never lie in
 // front of their destinations and nobody else touches its column, so reading a few
-// tokens ahead of the writes keeps the move in place and free of barriers.
+// tokens ahead of the writes keeps the move in place and free of barriers. Rows of 64 to 512
+// bytes here and there, bound by their latency: 92 layers of 8 heads of 128 E4M3, 32 sequences,
+// 60 MB, 16.5 us (two columns a thread 17.4, four 20.3).
 constexpr int CP_THREADS = 256;
 constexpr int CP_AHEAD = 8;              // tokens read before the first of them is written
 

@@ -19,7 +19,9 @@
 // descending, id ascending). Rows where more elements than the list holds reach
 // the bound, or that hold NaN or +infinity, take n rounds over the slice instead.
 //
-// Bound by HBM for many rows (each logit is read once), by latency for a few.
+// Bound by HBM for many rows (each logit is read once): 2048 rows of 100003 fp32, 819 MB, 159 us,
+// 5.1 TB/s (blocks of 512 threads: 187 us; smaller ones hide each other's ends of rows). By
+// latency for a few: one row of 131072 bf16 with 20 alternatives 9.6 us.
 #include <cooperative_groups.h>
 
 #include "kernels.cuh"
