@@ -178,8 +178,9 @@ moe_status moe_tree_attention(const moe_kv_cache* cache, const moe_kv_batch* bat
     a.status = static_cast<DevStatus*>(ws);
     void* partials = static_cast<char*>(ws) + sizeof(DevStatus);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return from_cuda(tree_attn_tiles_apply(a) ? launch_tree_attn_tiles(a, partials, st)
-                                              : launch_tree_attn_small(a, partials, st));
+    return from_cuda(tree_attn_wide_apply(a)    ? launch_tree_attn_wide(a, partials, st)
+                     : tree_attn_tiles_apply(a) ? launch_tree_attn_tiles(a, partials, st)
+                                                : launch_tree_attn_small(a, partials, st));
 }
 
 void moe_inject_attention_timeout(int n_calls) { tree_attn_inject_stall(n_calls > 0 ? n_calls : 0); }

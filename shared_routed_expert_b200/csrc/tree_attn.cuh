@@ -396,10 +396,58 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, const Partials& p, i
     if (a.lse != nullptr && lane == 0) a.lse[row * a.n_q + head] = lse_of(m, l);
 }
 
-constexpr int kSmallBlocks = 320;        // most blocks of the 16- to 64-row kernel
-constexpr int kSmallRows = 64;
-constexpr int kTileBlocks = 160;         // most blocks of the 256-row kernel
+// pairs of fp32 in one register pair: one instruction for two multiply-adds or additions
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// A row of an item again, key by key (a rare path, kept out of the main code's registers)
+template <int D, bool F8>
+__device__ __noinline__ void redo_row(const AttnArgs& a, const Cursor& c, int i, int head, int lo, int hi, float* o, float* ml,
+                                      int lane) {
+    constexpr int EPL = D / 32;
+    float q[EPL], acc[EPL], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        q[j] = bf16_to_f32(a.q[(c.s.row0 + i) * a.q_stride + head * D + lane * EPL + j]);
+        acc[j] = 0.f;
+    }
+    attend_row<EPL, F8>(a, c.b, c.s, i, c.h, q, lo, hi, m, l, acc, lane);
+    if (o != nullptr) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) o[lane * EPL + j] = acc[j];
+        if (lane == 0) {
+            ml[0] = m;
+            ml[1] = l;
+        }
+    } else {
+        const long long row = c.s.row0 + i;
+        const float inv = l == 0.f ? 0.f : __fdividef(a.c.v_scale, l);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            a.out[row * a.out_stride + head * D + lane * EPL + j] = f32_to_bf16(l == 0.f ? 0.f : acc[j] * inv);
+        if (a.lse != nullptr && lane == 0) a.lse[row * a.n_q + head] = lse_of(m, l);
+    }
+}
+
+constexpr int kSmallBlocks = 320;        // most blocks of the 16- or 32-row kernel
+constexpr int kSmallRows = 32;
+constexpr int kTileBlocks = 160;         // most blocks of the 256- and 128-row kernels
 constexpr int kTileRows = 256;
+constexpr int kWideRows = 128;           // ... of heads of 256 dimensions
 
 cudaError_t launch_tree_attn_small(const AttnArgs& a, void* partials, cudaStream_t st);
 cudaError_t launch_tree_attn_join(const AttnArgs& a, int M, Partials p, int blocks, cudaStream_t st);
@@ -411,6 +459,8 @@ bool make_kv_map(CUtensorMap* m, const AttnArgs& a, bool v, int box_rows);
 void tree_attn_inject_stall(int n_calls);
 bool tree_attn_take_stall();
 bool tree_attn_tiles_apply(const AttnArgs& a);
+bool tree_attn_wide_apply(const AttnArgs& a);
 cudaError_t launch_tree_attn_tiles(const AttnArgs& a, void* partials, cudaStream_t st);
+cudaError_t launch_tree_attn_wide(const AttnArgs& a, void* partials, cudaStream_t st);
 
 }  // namespace sre

@@ -1,8 +1,8 @@
 // Attention over a paged cache for few query rows per kv head (decoding, short drafts):
 // bound by reading the cache once.
 //
-// Flash decoding with warp-level matrix instructions: a block takes tiles of M = 16, 32
-// or 64 packed query rows and runs along its share of the key axis (tree_attn.cuh). Its 8
+// Flash decoding with warp-level matrix instructions: a block takes tiles of M = 16
+// or 32 packed query rows and runs along its share of the key axis (tree_attn.cuh). Its 8
 // warps form 8 / WM groups of WM warps; the groups take chunks of CK keys in turn, each
 // warp 16 rows, with its own running maximum and sum, so groups meet only at the end of an
 // item. Each group has a ring of its own in shared memory that its first warp fills by TMA
@@ -699,11 +699,7 @@ template <int D, bool F8>
 cudaError_t launch_d(const AttnArgs& a, void* partials, int sms, cudaStream_t st) {
     // rows of a tile: the smallest that holds a sequence's rows
     const long long rows = static_cast<long long>(a.c.max_new) * a.group;
-    if (rows <= 16) return launch_cfg<D, F8, 1>(a, partials, sms, st);
-    if constexpr (D == 256) {                                      // (narrower heads take tree_attn_tiles.cu then)
-        if (rows > 32) return launch_cfg<D, F8, 4>(a, partials, sms, st);
-    }
-    return launch_cfg<D, F8, 2>(a, partials, sms, st);
+    return rows <= 16 ? launch_cfg<D, F8, 1>(a, partials, sms, st) : launch_cfg<D, F8, 2>(a, partials, sms, st);
 }
 
 }  // namespace

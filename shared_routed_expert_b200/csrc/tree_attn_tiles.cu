@@ -67,53 +67,6 @@ struct TileParams {
     bool stall;                          // testing: no loads
 };
 
-// pairs of fp32 in one register pair: one instruction for two multiply-adds or additions
-__device__ __forceinline__ uint64_t pair2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-// A row of an item again, key by key (a rare path, kept out of the main code's registers)
-template <int D, bool F8>
-__device__ __noinline__ void redo_row(const AttnArgs& a, const Cursor& c, int i, int head, int lo, int hi, float* o, float* ml,
-                                      int lane) {
-    constexpr int EPL = D / 32;
-    float q[EPL], acc[EPL], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        q[j] = bf16_to_f32(a.q[(c.s.row0 + i) * a.q_stride + head * D + lane * EPL + j]);
-        acc[j] = 0.f;
-    }
-    attend_row<EPL, F8>(a, c.b, c.s, i, c.h, q, lo, hi, m, l, acc, lane);
-    if (o != nullptr) {
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) o[lane * EPL + j] = acc[j];
-        if (lane == 0) {
-            ml[0] = m;
-            ml[1] = l;
-        }
-    } else {
-        const long long row = c.s.row0 + i;
-        const float inv = l == 0.f ? 0.f : __fdividef(a.c.v_scale, l);
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            a.out[row * a.out_stride + head * D + lane * EPL + j] = f32_to_bf16(l == 0.f ? 0.f : acc[j] * inv);
-        if (a.lse != nullptr && lane == 0) a.lse[row * a.n_q + head] = lse_of(m, l);
-    }
-}
-
 template <int D, bool F8>
 __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kernel(const __grid_constant__ TileParams p) {
     using S = Tile<D, F8>;

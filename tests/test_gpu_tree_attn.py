@@ -413,6 +413,57 @@ def test_output_over_the_queries_beside_values_without_a_number(n, n_q, d, kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,ctx,n_q,n_kv,page", [([600, 33], [1700, 0], 4, 1, 16), ([9, 9, 1], [3000, 129, 640], 16, 2, 64),
+                                                 ([257, 64], [127, 128], 2, 2, 256), ([40], [1], 12, 12, 32)])
+def test_many_rows_of_wide_heads(n, ctx, n_q, n_kv, page, kv):
+    """Heads of 256 dimensions: several tiles, cut items, scores whose maximum keeps rising (keys that
+    grow along the sequence, so that sums are rescaled), chains and trees."""
+    P = Paged(n, ctx, n_kv, 256, page, kv, seed=27, rows=sum(n) + 2)
+    q = make_q(P, n_q, std=0.7)
+    for b in range(len(n)):
+        pg, sl = P.slots(b)
+        i = torch.arange(ctx[b] + n[b], device=DEV)
+        ramp = ((i // 100 + 1).float() * 4).clamp(max=64)
+        for h in range(n_kv):                              # one dimension rises by steps
+            row = ramp if not P.f8 else ramp.to(torch.float8_e4m3fn).view(torch.uint8)
+            P.k[pg, h, sl, 5] = row.to(P.k.dtype) if not P.f8 else row
+    q.view(P.T, n_q, 256)[:, :, 5] = q.view(P.T, n_q, 256)[:, :, 5].abs() + 1
+    for sets in (None, [w for a in n for w in tree_sets(a, 12)] if max(n) <= 300 else None):
+        out, lse, st = run(P, q, n_q, sets)
+        assert st == _lib.MOE_OK
+        check(P, q, n_q, out, lse, sets)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_extreme_scores_bad_pages_and_waits_of_wide_heads(kv):
+    n_q = 4
+    P = Paged([40, 12], [400, 9], 1, 256, 16, kv, seed=28)
+    q = make_q(P, n_q, std=60.0)
+    out, lse, _ = run(P, q, n_q)
+    check(P, q, n_q, out, lse)
+    for scale in (0.0, -0.125):
+        q = make_q(P, n_q)
+        out, lse, _ = run(P, q, n_q, scale=scale)
+        check(P, q, n_q, out, lse, scale=scale)
+    sets = [0] * 20 + tree_sets(40, 13)[20:] + tree_sets(12, 14)     # rows that see the prefix alone
+    out, lse, _ = run(P, q, n_q, sets)
+    check(P, q, n_q, out, lse, sets)
+    cache, batch = P.handles(m)
+    ws = m.alloc_tree_attention_workspace(cache, n_q, P.T)
+    _lib.moe_inject_attention_timeout(1)
+    m.moe_tree_attention(cache, batch, n_q, q, out, ws, lse=lse)
+    assert m.moe_get_status(ws) == _lib.MOE_ERR_TIMEOUT
+    ws.zero_()
+    P.table[0, 3] = P.pages
+    m.moe_tree_attention(cache, batch, n_q, q, out, ws, lse=lse)
+    assert m.moe_get_status(ws) == _lib.MOE_ERR_DEVICE
+    i0, i1 = torch.arange(440, device=DEV), torch.arange(21, device=DEV)
+    P.table[0, 3] = 0                                      # (any page: hidden in the reference)
+    ref, _, to, _ = attention_ref(P, q, n_q, None, None, [i0 // 16 == 3, i1 < 0])
+    assert float(((out.view(P.T, n_q, 256).double() - ref).abs() - to).max()) <= 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("n,d", [(1, 128), (3, 256), (30, 128), (5, 64)])
 def test_waits_that_run_out_are_reported(n, d, kv):
     """Loads that never come: the bounded waits run out, the kernels return and say so, and a
