@@ -458,6 +458,8 @@ bool make_kv_map(CUtensorMap* m, const AttnArgs& a, bool v, int box_rows);
 // testing hook: the next n calls run with loads that are never issued and a ~10 ms wait limit
 void tree_attn_inject_stall(int n_calls);
 bool tree_attn_take_stall();
+// whether a call is so short that the 16- or 32-row kernel takes it whatever its rows
+bool tree_attn_short(const AttnArgs& a);
 bool tree_attn_tiles_apply(const AttnArgs& a);
 bool tree_attn_wide_apply(const AttnArgs& a);
 cudaError_t launch_tree_attn_tiles(const AttnArgs& a, void* partials, cudaStream_t st);

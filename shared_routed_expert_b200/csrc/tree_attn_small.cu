@@ -704,6 +704,19 @@ cudaError_t launch_d(const AttnArgs& a, void* partials, int sms, cudaStream_t st
 
 }  // namespace
 
+// A block here has done its first chunk before the tiles of the other kernels have begun (they
+// allocate TMEM, fill a pipeline of steps and have a second launch for the join), so a call that
+// keeps each block busy for no more than a few units is done sooner here: 14 sequences of 21 to 65
+// tokens of 10 heads over 2 kv heads, E4M3, 14 us here, 28 us there; 2 sequences of 49 and 149 tokens of
+// 12 heads behind 1278 keys 24 and 39 us; 3 sequences of 266 to 800 tokens of 4 heads behind
+// 1515 keys, 10 units a block, 60 us and 41 us there. The contexts are on the device; what the
+// page table can hold bounds them.
+bool tree_attn_short(const AttnArgs& a) {
+    const long long tiles = (static_cast<long long>(a.T) * a.group / 32 + a.c.B) * a.c.n_kv;
+    const long long units = (static_cast<long long>(a.c.max_pages) << a.c.page_shift) / 256 + 3;
+    return tiles * units <= 4 * 296;
+}
+
 cudaError_t launch_tree_attn_small(const AttnArgs& a, void* partials, cudaStream_t st) {
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);

@@ -41,6 +41,9 @@ constexpr int kTileExtra = 4;            // what an item costs besides its steps
 // other kernel (tree_attn_small.cu) a pass over K and V in shared memory: 32 sequences of 4 rows
 // of 96 heads (48 rows a kv head), 566 MB of bf16 cache: 107 us here, 195 us there.
 constexpr int kTileLeastRows = 32;
+// Units of the shortest share: with 8, 12 sequences of 30 to 90 tokens of 20 heads over 4 kv heads behind up
+// to 153 keys, E4M3, take 40 us instead of 29
+constexpr int kTileLeastShare = 3;
 constexpr int kInfo = 8;                 // steps whose key masks are kept (the producer is at most 6 ahead)
 
 template <int D, bool F8>
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
     }
     ScanThread me;
     const long long W = scan_units(a, G, scan, me);
-    const Shares shares(W, gridDim.x, 4 + kTileExtra);
+    const Shares shares(W, gridDim.x, kTileLeastShare);
     if (threadIdx.x == 0) p.part.items[blockIdx.x].parts = 0;
     if (static_cast<int>(blockIdx.x) >= shares.count) return;
     const long long x0 = shares.begin(blockIdx.x), x1 = shares.begin(blockIdx.x + 1);
@@ -704,7 +707,7 @@ cudaError_t launch_tiles(const AttnArgs& a, void* partials, int sms, cudaStream_
 }  // namespace
 
 bool tree_attn_tiles_apply(const AttnArgs& a) {
-    return a.head_dim <= 128 && static_cast<long long>(a.c.max_new) * a.group > kTileLeastRows;
+    return a.head_dim <= 128 && static_cast<long long>(a.c.max_new) * a.group > kTileLeastRows && !tree_attn_short(a);
 }
 
 cudaError_t launch_tree_attn_tiles(const AttnArgs& a, void* partials, cudaStream_t st) {

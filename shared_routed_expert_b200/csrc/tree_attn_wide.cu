@@ -30,6 +30,7 @@ constexpr int kWideExtra = 4;            // what an item costs besides its steps
 // kv head), 568 MB of bf16 cache 105 us here, 183 us there, E4M3 147 and 202 us; of 7 rows (28), two
 // passes there, 109 and 116 us there.
 constexpr int kWideLeastRows = 32;
+constexpr int kWideLeastShare = 3;       // units of the shortest share
 constexpr int kInfo = 8;                 // steps whose key masks are kept (the producer is at most 4 ahead)
 
 template <bool F8>
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(F8 ? WD_THREADS_F8 : WD_THREADS, 1) wide_kerne
     }
     ScanThread me;
     const long long W = scan_units(a, G, scan, me);
-    const Shares shares(W, gridDim.x, 4 + kWideExtra);
+    const Shares shares(W, gridDim.x, kWideLeastShare);
     if (threadIdx.x == 0) p.part.items[blockIdx.x].parts = 0;
     if (static_cast<int>(blockIdx.x) >= shares.count) return;
     const long long x0 = shares.begin(blockIdx.x), x1 = shares.begin(blockIdx.x + 1);
@@ -587,7 +588,7 @@ cudaError_t launch_wide(const AttnArgs& a, void* partials, int sms, cudaStream_t
 }  // namespace
 
 bool tree_attn_wide_apply(const AttnArgs& a) {
-    return a.head_dim == 256 && static_cast<long long>(a.c.max_new) * a.group > kWideLeastRows;
+    return a.head_dim == 256 && static_cast<long long>(a.c.max_new) * a.group > kWideLeastRows && !tree_attn_short(a);
 }
 
 cudaError_t launch_tree_attn_wide(const AttnArgs& a, void* partials, cudaStream_t st) {
