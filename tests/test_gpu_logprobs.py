@@ -183,3 +183,14 @@ def test_graph_replay_and_repeat_bit_for_bit():
     a = run(x, t, 20)
     for u, v in zip(a, (lp, ent, ids, top)):
         assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,n", [(12, 32003, 32), (160, 16385, 1), (222, 17011, 5), (9, 8193, 1), (1, 4097, 7)])
+def test_rows_over_several_blocks(T, V, n, dt):
+    """Slices down to 4096 elements, and the single alternative."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T + V)
+    x = (torch.randn(T, V, generator=g, device=DEV) * 3).to(torch.bfloat16 if dt == "bf16" else torch.float32)
+    targets = torch.randint(0, V, (T,), generator=g, device=DEV, dtype=torch.int32)
+    check(x, targets, n, run(x, targets, n))
