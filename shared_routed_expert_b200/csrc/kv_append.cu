@@ -235,7 +235,9 @@ void append_ki(const AppendArgs& a, const KvView& c, bool f8, cudaStream_t st) {
 
 template <int LPH, int SH>
 void append_sh(const AppendArgs& a, const KvView& c, bool f8, cudaStream_t st) {
-    constexpr int KI = LPH == 32 ? 8 : 4;      // heads per warp: 8, or 16 of 64 dimensions
+    // 4 instructions' worth of heads a warp: 16, 8 or 4 of 64, 128 or 256 dimensions (of 256, 3000 tokens of
+    // 112 heads: 73 us, with 8 heads a warp 82, with 2 88)
+    constexpr int KI = 4;
     // a decode batch that the SMs hold at once takes half as many heads a warp: a shorter chain
     // (1 token of 112 heads 2.9 against 3.4 us, 64 tokens 4.1 against 4.8 us), while more heads
     // share what is looked up per token in a prefill chunk (5949 tokens 78 against 100 us)
