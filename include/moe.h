@@ -438,7 +438,8 @@ moe_status moe_qk_norm_rope_append(const moe_kv_cache* cache, const moe_kv_batch
  * n_q a multiple of n_kv, n_q <= 1024; row strides multiples of 8; softmax_scale
  * and softmax_scale * k_scale * log2(e) finite. The result does not depend on the
  * timing of the run (no atomics in the sums), but a row's rounding may depend on
- * the other sequences of the batch. */
+ * the other sequences of the batch and on the page table's width (kernels and
+ * splits are chosen by T, B, max_new and max_pages). */
 moe_status moe_tree_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, int32_t T, int32_t n_q,
                               float softmax_scale, const void* q, int64_t q_stride, const uint64_t* tree_mask,
                               int32_t mask_words, void* out, int64_t out_stride, float* lse, void* ws,
