@@ -454,6 +454,11 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                     if (!ok) break;
                     sp ^= 1u;
                     ptx::tc_fence_after();
+                    if (sub * 32 >= rows) {                        // no rows here: what lies in P reaches nobody's O
+                        ptx::tc_fence_before();
+                        ptx::mbar_arrive(&p_ready[h]);
+                        continue;
+                    }
                     const int c0 = st * TK;
                     const uint32_t* word = info[(step_no + st - lo) % kInfo];
                     const bool masked = c0 + TK > clear || (word[0] & word[1] & word[2] & word[3]) != 0xFFFFFFFFu;

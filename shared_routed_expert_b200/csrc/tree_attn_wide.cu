@@ -404,6 +404,11 @@ __global__ void __launch_bounds__(F8 ? WD_THREADS_F8 : WD_THREADS, 1) wide_kerne
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 ptx::tc_fence_after();
+                if (warp * 32 >= rows) {                           // no rows here: what lies in P reaches nobody's O
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(&p_ready[b]);
+                    continue;
+                }
                 const int c0 = st * TK;
                 const uint32_t* word = info[steps % kInfo];
                 const bool masked = c0 + TK > clear || (word[0] & word[1] & word[2] & word[3]) != 0xFFFFFFFFu;
