@@ -66,6 +66,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// From reference `from` down to a larger one, base 2. Bounded: a sum times it stays finite where its power is
+// 0 (a mask of the type's lowest value overflows it to -infinity, and -infinity * 0 is NaN).
+__device__ __forceinline__ float fall(float from, float to) { return fmaxf((from - to) * kLog2e, -1000.0f); }
+
 // pairs of fp32 in one register pair
 __device__ __forceinline__ uint64_t pair2(float a, float b) {
     uint64_t r;
@@ -229,7 +233,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(int V, const ch
         const float m2 = fmaxf(m, gm);
         const float ref = m2 == -INFINITY ? 0.0f : m2;
         if (gm > m) {
-            const float shift = m == -INFINITY ? 0.0f : (m - ref) * kLog2e;   // <= 0
+            const float shift = m == -INFINITY ? 0.0f : fall(m, ref);   // <= 0
             const float a = exp2_fast(shift);
             const float l = rest.l + best.l;
             rest.t = (rest.t + best.t + l * shift) * a;
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(int V, const ch
     }
     float l = rest.l + best.l, tt = rest.t + best.t;
     {
-        const float shift = m == -INFINITY ? 0.0f : (m - bref) * kLog2e;
+        const float shift = m == -INFINITY ? 0.0f : fall(m, bref);
         const float a = exp2_fast(shift);
         tt = (tt + l * shift) * a;
         l *= a;
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(int V, const ch
             float ol = o.y;
             if (o.x == M && !out) out = true;                      // the one maximum left out
             else ol += 1.0f;
-            const float shift = (o.x - M) * kLog2e, a = exp2_fast(shift);
+            const float shift = fall(o.x, M), a = exp2_fast(shift);
             TT += (o.z + ol * shift) * a;
             L += ol * a;
         }

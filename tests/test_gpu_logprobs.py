@@ -194,3 +194,27 @@ def test_rows_over_several_blocks(T, V, n, dt):
     x = (torch.randn(T, V, generator=g, device=DEV) * 3).to(torch.bfloat16 if dt == "bf16" else torch.float32)
     targets = torch.randint(0, V, (T,), generator=g, device=DEV, dtype=torch.int32)
     check(x, targets, n, run(x, targets, n))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("hidden", ["lowest", -1e38, -1e34, -1e30, -3e4])
+@pytest.mark.parametrize("T,V,n", [(16, 40000, 8), (300, 5003, 3), (8, 131072, 20), (16, 100, 0)])
+def test_rows_masked_with_large_negative_numbers(T, V, n, hidden, dt):
+    """Masks that are numbers: whole threads, slices and groups hold nothing else, in front of the tokens that
+    are left, behind them, or on both sides. (A masked token's term is below 2^-1000, its logarithm's error as
+    everywhere: the tolerances of `check`, where only terms with |d| < 24 count.)"""
+    t = torch.bfloat16 if dt == "bf16" else torch.float32
+    g = torch.Generator(device=DEV)
+    g.manual_seed(V)
+    x = (torch.randn(T, V, generator=g, device=DEV) * 3).to(t)
+    low = torch.finfo(t).min if hidden == "lowest" else hidden
+    i = torch.arange(V, device=DEV)
+    keep = [i < 5, i >= V - 5, i == V // 2, (i > V // 3) & (i < V // 3 + 1000), i % 97 == 3, i < V // 2, i >= V // 2, i < 0]
+    for r in range(T):
+        x[r, ~keep[r % 8]] = low
+    if hidden == "lowest":
+        x[0, ~keep[0]] = 0.45 * low                         # a difference that overflows in base 2 alone
+        x[0, V - 1] = -0.45 * low
+    targets = torch.randint(0, V, (T,), generator=g, device=DEV).int()
+    targets[::2] = x[::2].argmax(1).int()
+    check(x, targets, n, run(x, targets, n))
