@@ -420,7 +420,8 @@ moe_status moe_qk_norm_rope_append(const moe_kv_cache* cache, const moe_kv_batch
  *              mask_words <= 64.
  *   out[t][h] = sum_j p_j v_j,  p = softmax_j(softmax_scale * q . k_j), in fp32
  *              (p is rounded to the matrix instructions' 16-bit operands in the
- *              product with v), rounded once to bf16
+ *              product with v: to bf16, or over E4M3 caches to fp16 with steps
+ *              of 2^-31 of the largest p or finer), rounded once to bf16
  *   lse[t][h] = ln sum_j exp(softmax_scale * q . k_j), fp32, or lse NULL
  * A row that sees nothing (or only scores of -infinity) gives zeros and -infinity.
  * Keys and values that a row does not see do not reach it, whatever they hold.

@@ -48,6 +48,17 @@ __device__ __forceinline__ float fast_exp2(float x) {
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2F = 0.6931471805599453f;
 
+// Exponents of P over E4M3 caches are raised by this much (of l and O with them), since P is fp16 there: the
+// running maximum may lie 2^8 below the row's, so P stays below 2^15, and the smallest step of a weight is
+// 2^-31 of the largest, not 2^-24 (a million keys of 2^-25 each would vanish from O, though not from l).
+// bf16 has the exponents of fp32.
+constexpr float kLift = 7.f;
+template <bool F8>
+__device__ __forceinline__ float lifted(float ref) {               // what a score's exponent is taken from
+    if constexpr (F8) return ref - kLift;
+    else return ref;
+}
+
 // ln sum 2^s from the maximum m (base 2) and l = sum 2^(s - m); -infinity for l = 0
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2F; }
 

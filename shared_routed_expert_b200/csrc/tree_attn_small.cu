@@ -23,7 +23,7 @@
 //   and V's 16-bit transposed loads return pairs of neighbouring dimensions that a byte
 //   permutation turns into pairs of keys.
 // The accumulators are rescaled only when a row's maximum grows by more than 2^8 (P stays
-// below 2^8, far from fp16's and bf16's limits).
+// below 2^8, or 2^15 over E4M3 caches, where fp16's range is used from its upper end: kLift).
 #include "kernels.cuh"
 #include "tc_ptx.cuh"
 #include "tree_attn.cuh"
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
                         o[n][3] *= f1;
                     }
                 }
-                const float ref0 = m0 == -INFINITY ? 0.f : m0 * sc0, ref1 = m1 == -INFINITY ? 0.f : m1 * sc1;
+                const float ref0 = m0 == -INFINITY ? 0.f : lifted<F8>(m0 * sc0), ref1 = m1 == -INFINITY ? 0.f : lifted<F8>(m1 * sc1);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     sacc[n][0] = fast_exp2(fmaf(sacc[n][0], sc0, -ref0));
@@ -507,8 +507,8 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
         }
 
         // ---- the warps' results meet in shared memory, maxima in base 2
-        m0 *= sc0;
-        m1 *= sc1;
+        m0 = lifted<F8>(m0 * sc0);
+        m1 = lifted<F8>(m1 * sc1);
 #pragma unroll
         for (int off = 1; off < 4; off <<= 1) {
             l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, off);

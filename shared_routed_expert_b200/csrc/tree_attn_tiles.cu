@@ -24,8 +24,8 @@
 // steps of 64 keys with two S (4950 us: a product of N = 64 takes as long as one of 128).
 // E4M3 caches: the boxes go to a ring of codes, from which warps 10 and 11 write K and V as
 // fp16 (exact) to the products' ring (2048 rows behind 8192 keys: 1088 us, bf16 910 us). Q rows are scaled by a power of two to fp16 (exact for
-// everything within 2^-28 of the row's largest entry) and P is fp16. (E4M3 operands would
-// need P in 4 significant bits.)
+// everything within 2^-28 of the row's largest entry) and P is fp16, raised by 2^7 (kLift). (E4M3
+// operands would need P in 4 significant bits.)
 #include "kernels.cuh"
 #include "tc_ptx.cuh"
 #include "tree_attn.cuh"
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                             }
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.f : m * scale;
+                    const float ref = m == -INFINITY ? 0.f : lifted<F8>(m * scale);
                     const uint64_t scale2 = pair2(scale, scale), ref2 = pair2(-ref, -ref);
                     uint64_t sum2[2] = {0, 0};
                     // P of keys 32 q .. goes where S of later keys was: columns 64 + 16 q ..
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(F8 ? TL_THREADS_F8 : TL_THREADS, 1) tiles_kern
                 if (!ok) break;
                 op ^= 1u;
                 ptx::tc_fence_after();
-                float m2 = l == 0.f ? -INFINITY : m * scale, f0 = 1.f, f1 = 0.f;
+                float m2 = l == 0.f ? -INFINITY : lifted<F8>(m * scale), f0 = 1.f, f1 = 0.f;
                 if (share) {
                     const int x = sub * 32 + lane;
                     if (h == 1) {

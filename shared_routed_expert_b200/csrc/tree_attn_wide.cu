@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(F8 ? WD_THREADS_F8 : WD_THREADS, 1) wide_kerne
                         }
                     }
                 }
-                const float ref = m == -INFINITY ? 0.f : m * scale;
+                const float ref = m == -INFINITY ? 0.f : lifted<F8>(m * scale);
                 const uint64_t scale2 = pair2(scale, scale), ref2 = pair2(-ref, -ref);
                 uint64_t sum2[2] = {0, 0};
 #pragma unroll
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(F8 ? WD_THREADS_F8 : WD_THREADS, 1) wide_kerne
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             ptx::tc_fence_after();
-            const float m2 = l == 0.f ? -INFINITY : m * scale;
+            const float m2 = l == 0.f ? -INFINITY : lifted<F8>(m * scale);
             const bool mine = warp * 32 + lane < rows;
             const int head = cur.h * a.group + rr - i * a.group;
             const long long row = s.row0 + i;
