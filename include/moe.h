@@ -388,7 +388,8 @@ typedef struct moe_kv_batch {
  * the q heads are normalised, rotated and written to q_out, the k heads the same
  * and written to the cache, the v heads written to the cache. fp32 arithmetic,
  * one rounding (to bf16, or to E4M3_rn_satfinite(value / scale)); the q rows and
- * bf16 keys are those of moe_qk_norm_rope bit for bit.
+ * bf16 keys are those of moe_qk_norm_rope bit for bit, but for an infinity in a
+ * dimension that does not rotate, which stays one here and gives NaN there.
  *   qkv        [T] rows of (n_q + 2*n_kv) * head_dim bf16, qkv_stride elements
  *              apart (q heads | k heads | v heads); not changed
  *   positions  [T] int32 rotation positions, each in [0, max_pos); drafted tree

@@ -179,7 +179,12 @@ __global__ void __launch_bounds__(AP_WARPS * 32, 4) append_kernel(const AppendAr
             widen8(raw[k], v);
             normed(v, w, true, u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = u[j] * co[j] + partner(u, j) * sn[j];
+            for (int j = 0; j < 8; ++j) {
+                const float o = partner(u, j);
+                // dimensions that do not rotate pass through whatever their value and that of what is offered
+                // to them, another dimension if SH is not 0 (0 * infinity; 0.7% of a prompt's time)
+                y[j] = turns[j / PS] ? u[j] * co[j] + o * sn[j] : u[j];
+            }
             *reinterpret_cast<uint4*>(dst + k * HPI * D) =
                 make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
         }
@@ -202,7 +207,6 @@ __global__ void __launch_bounds__(AP_WARPS * 32, 4) append_kernel(const AppendAr
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float o = partner(u, j);
-            // dimensions that do not rotate pass through whatever their value (0 * infinity)
             y[j] = turns[j / PS] ? u[j] * co[j] + o * sn[j] : u[j];
         }
         if (!real || (!is_q && slot < 0)) continue;

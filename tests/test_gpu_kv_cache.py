@@ -1,5 +1,6 @@
 """The append to the paged cache, the move of accepted drafts inside it, and a speculative decoding
 step made of append, attention, log probabilities and move."""
+import dataclasses
 import math
 
 import numpy as np
@@ -376,3 +377,56 @@ def test_append_and_compact_in_a_graph():
     torch.cuda.synchronize()
     assert torch.equal(gk.view(torch.int16), P.k.view(torch.int16)) and torch.equal(gv.view(torch.int16), P.v.view(torch.int16))
     assert not torch.equal(gk.view(torch.int16), k0.view(torch.int16))
+
+
+@pytest.mark.parametrize("n_q", [4, 24, 33])
+@pytest.mark.parametrize("T", [13, 700])
+@pytest.mark.parametrize("d,rot", [(128, 24), (128, 64), (64, 36), (64, 12), (64, 8), (256, 128)])
+def test_append_keeps_the_bits_of_the_norm_and_rotation_beside_infinities(d, rot, T, n_q):
+    """q rows and bf16 keys equal moe_qk_norm_rope's bit for bit, whichever warp has the head: negative
+    zeros, infinities and NaN in one dimension of a row, weights that are infinite or zero, and rows so small
+    that the mean square vanishes (eps 0). Where a dimension does not rotate, an infinity stays one."""
+    n_kv = 3 if n_q % 3 == 0 else 2
+    for eps in (1e-5, 0.0):
+        P = Paged([T], [5], n_kv, d, 16, "bf16", seed=30)
+        cfg, inp = attn_inputs(T, n_q, n_kv, d, rot, 900, 12)
+        cfg = dataclasses.replace(cfg, eps=eps)
+        cache, batch = P.handles(m)
+        x = inp["qkv"].view(T, n_q + 2 * n_kv, d)
+        x[::2, :, 1::3] = -0.0
+        x[1, :, d - 3], x[2, :, d - 6], x[3, :, rot // 2 + 1], x[4, :, 0] = math.inf, math.nan, -math.inf, math.inf
+        x[5] = torch.where(x[5] == 0, x[5], 1e-30 * torch.sign(x[5]))
+        for w in (inp["q_w"], inp["k_w"]):
+            w[d - 2], w[1], w[d - 5] = math.inf, 0.0, -1.0
+        both = inp["qkv"].clone()
+        q_out = torch.empty(T, n_q * d, dtype=torch.bfloat16, device=DEV)
+        m.moe_qk_norm_rope_append(cache, batch, n_q, rot, eps, inp["qkv"], inp["pos"], inp["q_w"], inp["k_w"],
+                                  inp["cos_sin"], q_out)
+        _lib.moe_qk_norm_rope(cfg, both, inp["pos"], inp["q_w"], inp["k_w"], inp["cos_sin"])
+        want = both.view(T, n_q + 2 * n_kv, d)[:, :n_q + n_kv].clone()
+        u = x[:, :n_q + n_kv].float()
+        u = u * torch.rsqrt(u.square().mean(-1, keepdim=True) + eps)
+        u = u * torch.cat([inp["q_w"].float().expand(n_q, d), inp["k_w"].float().expand(n_kv, d)])
+        stays = torch.isinf(u) & (torch.arange(d, device=DEV) >= rot)
+        assert bool(stays.any()) and bool(torch.isnan(want[stays]).all())
+        want[stays] = u[stays].to(torch.bfloat16)
+        pg, sl = P.slots(0)
+        got = torch.cat([q_out.view(T, n_q, d), P.k[pg[5:], :, sl[5:]]], 1)
+        assert bool(torch.isnan(want).any()) and bool((want == 0).any())
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        fine = ~torch.isnan(want)
+        assert torch.equal(got.view(torch.int16)[fine], want.view(torch.int16)[fine])
+
+
+def test_append_without_norms_passes_infinities_through():
+    """Heads without a norm: dimensions that do not rotate keep their value, whatever it is."""
+    P = Paged([9], [5], 2, 64, 16, "bf16", seed=31)
+    cfg, inp = attn_inputs(9, 4, 2, 64, 12, 64, 13)
+    cache, batch = P.handles(m)
+    x = inp["qkv"].view(9, 8, 64)
+    x[1, :, 20], x[2, :, 63], x[3, :, 40] = math.inf, -0.0, -math.inf
+    q_out = torch.empty(9, 4 * 64, dtype=torch.bfloat16, device=DEV)
+    m.moe_qk_norm_rope_append(cache, batch, 4, 12, cfg.eps, inp["qkv"], inp["pos"], None, None, inp["cos_sin"], q_out)
+    pg, sl = P.slots(0)
+    got = torch.cat([q_out.view(9, 4, 64), P.k[pg[5:], :, sl[5:]]], 1)[..., 12:].contiguous()
+    assert torch.equal(got.view(torch.int16), x[:, :6, 12:].contiguous().view(torch.int16))
