@@ -106,6 +106,33 @@ __device__ __forceinline__ void attend_row(const AttnArgs& a, int b, const SeqIn
     }
 }
 
+// Whether one of the keys [lo, hi) that a row (token i of the sequence; -1: one that sees no new token) does
+// not see has a value with an infinity or NaN, a lane per key. If none has, a NaN in the row's result is its own, and there is nothing to
+// compute again (one NaN among 4000 cached values, seen by all rows, made calls 4 to 180 times as long).
+template <int D, bool F8>
+__device__ __forceinline__ bool hides_infinities(const AttnArgs& a, int b, const SeqInfo& s, int i, int kv_head, int lo, int hi,
+                                              int lane) {
+    // (a row sees every cached token, in a chain the new ones up to itself too)
+    for (int c0 = max(lo, a.mask != nullptr ? s.ctx : s.ctx + i + 1); c0 < hi; c0 += 32) {
+        const int c = c0 + lane;
+        bool found = false;
+        if (c < hi && (i < 0 || !sees_new(a, s.row0 + i, i, c - s.ctx))) {
+            const long long off = slot_offset(a.c, b, c, kv_head);
+            for (int j = 0; off >= 0 && j < D * (F8 ? 1 : 2) / 16 && !found; ++j) {
+                const uint4 v = *reinterpret_cast<const uint4*>(a.c.v + off + 16 * j);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (F8) found |= __vcmpeq4(w[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+                    else found |= (w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u;
+                }
+            }
+        }
+        if (__any_sync(0xFFFFFFFFu, found)) return true;
+    }
+    return false;
+}
+
 // ---- splitting the work
 // An item is (sequence, kv head, tile of M query rows); the rows of a kv head are
 // packed token-major, row r being token r / group, query head r % group. An item takes
@@ -425,9 +452,24 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// Of the lanes `lanes`, those whose row's NaN may come from a value that it does not see (the lanes hold rows
+// of the item in order, i their tokens).
+template <int D, bool F8>
+__device__ __noinline__ uint32_t spoiled_lanes(const AttnArgs& a, const Cursor& c, int i, uint32_t lanes, int lo, int hi, int lane) {
+    // first for a row that sees no more than any of them: mostly there is no such value
+    const int first = __shfl_sync(0xFFFFFFFFu, i, __ffs(lanes) - 1);
+    if (!hides_infinities<D, F8>(a, c.b, c.s, a.mask != nullptr ? -1 : first, c.h, lo, hi, lane)) return 0;
+    uint32_t yes = 0;
+#pragma unroll 1
+    for (uint32_t rest = lanes; rest; rest &= rest - 1) {
+        const int src = __ffs(rest) - 1;
+        if (hides_infinities<D, F8>(a, c.b, c.s, __shfl_sync(0xFFFFFFFFu, i, src), c.h, lo, hi, lane)) yes |= 1u << src;
+    }
+    return yes;
+}
 // A row of an item again, key by key (a rare path, kept out of the main code's registers)
 template <int D, bool F8>
-__device__ __noinline__ void redo_row(const AttnArgs& a, const Cursor& c, int i, int head, int lo, int hi, float* o, float* ml,
+__device__ __forceinline__ void redo_row(const AttnArgs& a, const Cursor& c, int i, int head, int lo, int hi, float* o, float* ml,
                                       int lane) {
     constexpr int EPL = D / 32;
     float q[EPL], acc[EPL], m = -INFINITY, l = 0.f;
@@ -451,6 +493,19 @@ __device__ __noinline__ void redo_row(const AttnArgs& a, const Cursor& c, int i,
         for (int j = 0; j < EPL; ++j)
             a.out[row * a.out_stride + head * D + lane * EPL + j] = f32_to_bf16(l == 0.f ? 0.f : acc[j] * inv);
         if (a.lse != nullptr && lane == 0) a.lse[row * a.n_q + head] = lse_of(m, l);
+    }
+}
+
+// The rows of the lanes `lanes` that spoiled_lanes names, again: into out, or (part_o and part_ml not null)
+// into the partial results from this warp's first row on
+template <int D, bool F8>
+__device__ __noinline__ void redo_rows(const AttnArgs& a, const Cursor& c, uint32_t lanes, int i, int head, int lo, int hi,
+                                       float* part_o, float* part_ml, int lane) {
+#pragma unroll 1
+    for (uint32_t rest = spoiled_lanes<D, F8>(a, c, i, lanes, lo, hi, lane); rest; rest &= rest - 1) {
+        const int src = __ffs(rest) - 1;
+        redo_row<D, F8>(a, c, __shfl_sync(0xFFFFFFFFu, i, src), __shfl_sync(0xFFFFFFFFu, head, src), lo, hi,
+                        part_o == nullptr ? nullptr : part_o + src * D, part_ml + src * 2, lane);
     }
 }
 

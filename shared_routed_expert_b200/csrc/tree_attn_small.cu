@@ -598,7 +598,8 @@ __global__ void __launch_bounds__(SM_THREADS, (Small<D, F8, WM>::BLOCKS_PER_SM))
             bool nan = false;
 #pragma unroll
             for (int j = 0; j < EPL; ++j) nan |= acc[j] != acc[j];
-            if (hi * S::SK > s.ctx && l == l && __any_sync(0xFFFFFFFFu, nan)) {
+            if (hi * S::SK > s.ctx && l == l && __any_sync(0xFFFFFFFFu, nan) &&
+                hides_infinities<D, F8>(a, cur.b, s, i, cur.h, lo * S::SK, min(hi * S::SK, keys), lane)) {
                 // 0 * infinity or NaN: a value that this row may not see; again, key by key
                 float q[EPL];
 #pragma unroll

@@ -514,7 +514,8 @@ __global__ void __launch_bounds__(F8 ? WD_THREADS_F8 : WD_THREADS, 1) wide_kerne
                     uint32_t x[32];
                     stays |= take(q, x);
                 }
-                stays &= l == l;
+                const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, mine && stays && l == l);
+                stays = lanes != 0 && (spoiled_lanes<D, F8>(a, cur, i, lanes, lo * TK, min(hi * TK, keys), lane) >> lane & 1);
             }
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
@@ -545,15 +546,10 @@ __global__ void __launch_bounds__(F8 ? WD_THREADS_F8 : WD_THREADS, 1) wide_kerne
             }
             // 0 * infinity or NaN: a value that the row may not see; again, key by key
             __syncwarp();
-            uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && nan && l == l && unseen);
-            while (again) {
-                const int src = __ffs(again) - 1;
-                again &= again - 1;
-                const int ri = __shfl_sync(0xFFFFFFFFu, i, src), rh = __shfl_sync(0xFFFFFFFFu, head, src);
-                const size_t sr = slot_row - lane + src;
-                redo_row<D, F8>(a, cur, ri, rh, lo * TK, min(hi * TK, keys), whole ? nullptr : p.part.o + sr * D, p.part.ml + sr * 2,
-                                lane);
-            }
+            const uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && nan && l == l && unseen);
+            if (again)
+                redo_rows<D, F8>(a, cur, again, i, head, lo * TK, min(hi * TK, keys), whole ? nullptr : p.part.o + (slot_row - lane) * D,
+                                 p.part.ml + (slot_row - lane) * 2, lane);
         }
     }
     __syncwarp();

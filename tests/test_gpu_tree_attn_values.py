@@ -1,13 +1,14 @@
-"""Attention over the paged cache at values that a long context brings: weights far below the largest over
-E4M3 caches."""
+"""Attention over the paged cache at values that a long context or a broken sequence brings: weights far
+below the largest over E4M3 caches, and values without a number that every row sees."""
 import math
 
 import pytest
 import torch
 
+import shared_routed_expert_b200 as m
 from shared_routed_expert_b200 import _lib, build
-from tests.serve_util import Paged, attention_ref
-from tests.test_gpu_tree_attn import run
+from tests.serve_util import Paged, attention_ref, mask_tensor, tree_sets
+from tests.test_gpu_tree_attn import make_q, run
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -47,3 +48,80 @@ def test_small_weights_over_e4m3_caches_count(B, n, n_q, n_kv, d, ctx, bits):
     keys = ctx + n
     assert float(((out.view(P.T, n_q, d).double() - ref).abs() - to).max()) <= keys * 2.0 ** -32
     assert float(((lse.double() - rl).abs() - tl).max()) <= 0
+
+
+def milliseconds(f):
+    f()
+    times = []
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    return min(times)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,ctx,n_q,n_kv,d,tree", [([1] * 64, [4000] * 64, 16, 2, 128, False), ([3] * 40, [3000] * 40, 8, 1, 64, True),
+                                                   ([40, 40], [6000, 5000], 24, 2, 128, True), ([300], [4000], 12, 1, 64, False),
+                                                   ([30] * 4, [5000] * 4, 8, 2, 256, False), ([60] * 4, [3000] * 4, 8, 2, 256, True)])
+def test_a_cached_value_without_a_number_costs_no_second_look(n, ctx, n_q, n_kv, d, tree, kv):
+    """A NaN among the cached values, which every row sees: it is in the rows' result, in its dimension alone,
+    and the call takes no longer for it (the rows have nothing to be computed again for)."""
+    P = Paged(n, ctx, n_kv, d, 64, kv, seed=41)
+    sets = [w for a in n for w in tree_sets(a, 15)] if tree else None
+    q = make_q(P, n_q)
+    cache, batch = P.handles(m)
+    ws = m.alloc_tree_attention_workspace(cache, n_q, P.T)
+    out, lse = torch.empty_like(q), torch.empty(P.T, n_q, device=DEV)
+    mask = mask_tensor(sets, 1) if tree else None
+
+    def call():
+        m.moe_tree_attention(cache, batch, n_q, q, out, ws, tree_mask=mask, lse=lse)
+
+    clean = milliseconds(call)
+    pg, sl = P.slots(0)
+    P.v[pg[3], 0, sl[3], 5] = 0x7F if P.f8 else math.nan
+    P.v[pg[ctx[0] - 1], 0, sl[ctx[0] - 1], d - 1] = 0x7F if P.f8 else math.nan
+    spoiled = milliseconds(call)
+    assert m.moe_get_status(ws) == _lib.MOE_OK
+    ref, rl, to, tl = attention_ref(P, q, n_q, sets)
+    got = out.view(P.T, n_q, d).double()
+    assert bool(torch.isnan(ref).any()) and torch.equal(torch.isnan(got), torch.isnan(ref))
+    assert float(torch.nan_to_num((got - ref).abs() - to, nan=0.0).max()) <= 0
+    assert float(((lse.double() - rl).abs() - tl).max()) <= 0
+    over = q.clone()
+    m.moe_tree_attention(cache, batch, n_q, over, over, ws, tree_mask=mask)
+    assert torch.equal(over.view(torch.int16), out.view(torch.int16))
+    assert spoiled < 2 * clean + 0.05, (clean, spoiled)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,ctx,n_q,n_kv,d,tree", [([14, 3], [90, 700], 8, 2, 128, True), ([40, 9], [300, 64], 12, 1, 128, True),
+                                                   ([100], [37], 4, 1, 64, False), ([50, 2], [500, 0], 2, 1, 256, True)])
+def test_cached_and_unseen_values_without_a_number(n, ctx, n_q, n_kv, d, tree, kv):
+    """NaN in a cached value and in a new token's that not every row sees, into a buffer and over the queries:
+    each row has NaN in the dimensions of the values it sees, and in no other."""
+    P = Paged(n, ctx, n_kv, d, 16, kv, seed=42)
+    sets = [w for a in n for w in tree_sets(a, 16)] if tree else None
+    pg, sl = P.slots(0)
+    nan = 0x7F if P.f8 else math.nan
+    P.v[pg[7], 0, sl[7], 5] = nan
+    at = ctx[0] + 4
+    P.v[pg[at], 0, sl[at], 9] = nan
+    q = make_q(P, n_q)
+    out, lse, st = run(P, q, n_q, sets)
+    assert st == _lib.MOE_OK
+    ref, rl, to, tl = attention_ref(P, q, n_q, sets)
+    got = out.view(P.T, n_q, d).double()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    assert bool(torch.isnan(ref[:n[0], 0, 5]).all()) and 0 < int(torch.isnan(ref[:n[0], 0, 9]).sum()) < n[0]
+    assert float(torch.nan_to_num((got - ref).abs() - to, nan=0.0).max()) <= 0
+    assert float(((lse.double() - rl).abs() - tl).max()) <= 0
+    cache, batch = P.handles(m)
+    ws = m.alloc_tree_attention_workspace(cache, n_q, P.T)
+    over = q.clone()
+    m.moe_tree_attention(cache, batch, n_q, over, over, ws, tree_mask=mask_tensor(sets, 2) if tree else None)
+    assert torch.equal(over.view(torch.int16), out.view(torch.int16))
