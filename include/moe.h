@@ -364,7 +364,9 @@ moe_status moe_qk_norm_rope(int32_t T, int32_t n_q, int32_t n_kv, int32_t head_d
  *               page are not read. Pages may be shared by sequences that only
  *               read them; a page that a call writes to belongs to one sequence.
  *   max_new     on the host: no sequence has more new rows than this
- * B at most 4096, T at most 2^20. The arrays are read when the kernels run, so a
+ * B at most 4096, T at most 2^20. Calls without rows (T 0) or, where a call has one
+ * entry per sequence, without sequences (B 0) do nothing, and their arrays of no
+ * elements may be NULL. The arrays are read when the kernels run, so a
  * captured graph replays with the lengths and pages of the time. Bad contents
  * (rows outside [0, T), negative lengths, more tokens than the table holds, page
  * ids outside [0, num_pages)) are never followed: the entry points say how each

@@ -109,14 +109,15 @@ moe_status moe_qk_norm_rope_append(const moe_kv_cache* cache, const moe_kv_batch
     if (rc != MOE_OK) return rc;
     if (T < 0 || !(eps >= 0.f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
     if (T > kMaxT) return MOE_ERR_UNSUPPORTED;
-    if (!qkv || !q_out || !at16(qkv) || !at16(q_out) || !at16(q_norm_w) || !at16(k_norm_w)) return MOE_ERR_INVALID_ARG;
+    if (!at16(qkv) || !at16(q_out) || !at16(q_norm_w) || !at16(k_norm_w)) return MOE_ERR_INVALID_ARG;
     const int64_t d = cache->head_dim;
     if (!row_ok(qkv_stride, (n_q + 2 * cache->n_kv) * d) || !row_ok(q_stride, n_q * d)) return MOE_ERR_INVALID_ARG;
-    if (qkv == q_out && qkv_stride != q_stride) return MOE_ERR_INVALID_ARG;
     if (!qk_norm_rope_supported(cache->head_dim, rot_dim)) return MOE_ERR_UNSUPPORTED;
-    if (rot_dim > 0 && (!positions || !at4(positions) || max_pos <= 0 || !cos_sin || !at16(cos_sin)))
-        return MOE_ERR_INVALID_ARG;
-    if (T == 0 || batch->B == 0) return MOE_OK;
+    if (rot_dim > 0 && (!at4(positions) || max_pos <= 0 || !cos_sin || !at16(cos_sin))) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;                                     // (arrays of no rows may be NULL)
+    if (!qkv || !q_out || (rot_dim > 0 && !positions)) return MOE_ERR_INVALID_ARG;
+    if (qkv == q_out && qkv_stride != q_stride) return MOE_ERR_INVALID_ARG;
+    if (batch->B == 0) return MOE_OK;
     return from_cuda(launch_append(view_of(*cache, *batch), cache->head_dim, cache->dtype == MOE_E4M3, T, n_q, rot_dim, eps,
                                    static_cast<const uint16_t*>(qkv), qkv_stride, positions, max_pos,
                                    static_cast<const uint16_t*>(q_norm_w), static_cast<const uint16_t*>(k_norm_w), cos_sin,
@@ -142,17 +143,17 @@ moe_status moe_tree_attention(const moe_kv_cache* cache, const moe_kv_batch* bat
     const float scale_log2 = softmax_scale * cache->k_scale * kLog2E;
     if (T < 0 || !std::isfinite(scale_log2)) return MOE_ERR_INVALID_ARG;
     if (T > kMaxT) return MOE_ERR_UNSUPPORTED;
-    if (!q || !out || !ws || !at16(q) || !at16(out) || !at4(lse) || (reinterpret_cast<uintptr_t>(ws) & 255u))
-        return MOE_ERR_INVALID_ARG;
+    if (!ws || !at16(q) || !at16(out) || !at4(lse) || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_INVALID_ARG;
     const int64_t width = static_cast<int64_t>(n_q) * cache->head_dim;
     if (!row_ok(q_stride, width) || !row_ok(out_stride, width)) return MOE_ERR_INVALID_ARG;
-    if (q == out && q_stride != out_stride) return MOE_ERR_INVALID_ARG;
-    if (tree_mask == nullptr ? mask_words != 0 : (mask_words < 1 || (reinterpret_cast<uintptr_t>(tree_mask) & 7u)))
+    if (mask_words < 0 || (tree_mask != nullptr && (mask_words < 1 || (reinterpret_cast<uintptr_t>(tree_mask) & 7u))))
         return MOE_ERR_INVALID_ARG;
     if (mask_words > 64) return MOE_ERR_UNSUPPORTED;
     if (tree_mask != nullptr && batch->max_new > 64 * mask_words) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < moe_tree_attention_workspace_size(cache, n_q, T)) return MOE_ERR_WORKSPACE;
-    if (T == 0 || batch->B == 0 || batch->max_new == 0) return MOE_OK;
+    if (T == 0) return MOE_OK;                                     // (arrays of no rows may be NULL)
+    if (!q || !out || (q == out && q_stride != out_stride) || (tree_mask == nullptr && mask_words != 0)) return MOE_ERR_INVALID_ARG;
+    if (batch->B == 0 || batch->max_new == 0) return MOE_OK;
     AttnArgs a;
     a.c = view_of(*cache, *batch);
     a.T = T;
@@ -191,12 +192,12 @@ moe_status moe_kv_compact(const moe_kv_cache* cache, const moe_kv_batch* batch, 
     moe_status rc = check_cache(cache);
     if (rc == MOE_OK) rc = check_batch(batch);
     if (rc != MOE_OK) return rc;
-    if (n_layers < 1 || max_accept < 1 || !accepted || !n_accepted || !at4(accepted) || !at4(n_accepted))
-        return MOE_ERR_INVALID_ARG;
+    if (n_layers < 1 || max_accept < 1 || !at4(accepted) || !at4(n_accepted)) return MOE_ERR_INVALID_ARG;
     if (n_layers > 4096 || max_accept > 1024) return MOE_ERR_UNSUPPORTED;
     const int esz = cache->dtype == MOE_BF16 ? 2 : 1;
     if (!stride_ok(layer_stride, n_layers, cache->head_dim, esz)) return MOE_ERR_INVALID_ARG;
-    if (batch->B == 0) return MOE_OK;
+    if (batch->B == 0) return MOE_OK;                              // (arrays of no sequences may be NULL)
+    if (!accepted || !n_accepted) return MOE_ERR_INVALID_ARG;
     return from_cuda(launch_compact(view_of(*cache, *batch), cache->head_dim * esz, n_layers,
                                     n_layers > 1 ? layer_stride * esz : 0, accepted, max_accept, n_accepted, bad_seqs,
                                     static_cast<cudaStream_t>(stream)));
@@ -209,11 +210,12 @@ moe_status moe_token_logprobs(int32_t T, int32_t V, int32_t dtype, const void* l
     if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
     if (T > kMaxT || V > (1 << 24) || top_n > 32 || row_stride >= (int64_t{1} << 40)) return MOE_ERR_UNSUPPORTED;
     if (top_n > V) return MOE_ERR_INVALID_ARG;
-    if (!logits || (reinterpret_cast<uintptr_t>(logits) & (dtype == MOE_BF16 ? 1u : 3u))) return MOE_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(logits) & (dtype == MOE_BF16 ? 1u : 3u)) return MOE_ERR_INVALID_ARG;
+    if (!at4(targets) || !at4(logprobs) || !at4(entropy) || !at4(top_ids) || !at4(top_logprobs)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;                                     // (arrays of no rows may be NULL)
+    if (!logits) return MOE_ERR_INVALID_ARG;
     if ((targets == nullptr) != (logprobs == nullptr)) return MOE_ERR_INVALID_ARG;
     if ((top_ids == nullptr) != (top_n == 0) || (top_logprobs == nullptr) != (top_n == 0)) return MOE_ERR_INVALID_ARG;
-    if (!at4(targets) || !at4(logprobs) || !at4(entropy) || !at4(top_ids) || !at4(top_logprobs)) return MOE_ERR_INVALID_ARG;
-    if (T == 0) return MOE_OK;
     return from_cuda(launch_logprobs(T, V, dtype == MOE_BF16, logits, row_stride, targets, top_n, logprobs, entropy,
                                      top_ids, top_logprobs, static_cast<cudaStream_t>(stream)));
 }

@@ -430,3 +430,26 @@ def test_append_without_norms_passes_infinities_through():
     pg, sl = P.slots(0)
     got = torch.cat([q_out.view(9, 4, 64), P.k[pg[5:], :, sl[5:]]], 1)[..., 12:].contiguous()
     assert torch.equal(got.view(torch.int16), x[:, :6, 12:].contiguous().view(torch.int16))
+
+
+def test_steps_without_rows_or_sequences():
+    """Tensors of no rows (whose address is NULL) through every call: nothing happens."""
+    k = torch.zeros(2, 1, 16, 128, dtype=torch.bfloat16, device=DEV)
+    cache = m.make_kv_cache(k, k.clone())
+    i32 = dict(dtype=torch.int32, device=DEV)
+    b16 = dict(dtype=torch.bfloat16, device=DEV)
+    for B in (0, 2):
+        batch = m.make_kv_batch(torch.zeros(B + 1, **i32), torch.zeros(B, **i32), torch.zeros(B, 1, **i32), 0)
+        ws = m.alloc_tree_attention_workspace(cache, 4, 0)
+        q = torch.empty(0, 4 * 128, **b16)
+        m.moe_qk_norm_rope_append(cache, batch, 4, 64, 1e-5, torch.empty(0, 6 * 128, **b16), torch.empty(0, **i32), None, None,
+                                  torch.ones(4, 64, device=DEV), q)
+        m.moe_tree_attention(cache, batch, 4, q, torch.empty_like(q), ws, lse=torch.empty(0, 4, device=DEV))
+        m.moe_tree_attention(cache, batch, 4, q, q, ws, tree_mask=torch.empty(0, 1, dtype=torch.int64, device=DEV))
+        m.moe_kv_compact(cache, batch, torch.zeros(B, 3, **i32), torch.zeros(B, **i32))
+        assert m.moe_get_status(ws) == _lib.MOE_OK
+    f = lambda *s: torch.empty(s, device=DEV)  # noqa: E731
+    m.moe_token_logprobs(f(0, 50), torch.empty(0, **i32), f(0), f(0), torch.empty(0, 3, **i32), f(0, 3))
+    m.moe_token_logprobs(f(0, 50), None, None, f(0))
+    torch.cuda.synchronize()
+    assert not bool(k.any())

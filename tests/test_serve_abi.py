@@ -134,6 +134,26 @@ def test_logprobs_refusals(L):
     assert logprobs(L, T=0) == OK
 
 
+def test_arrays_without_elements_may_be_null(L):
+    """An empty tensor's address is NULL: a step without rows or sequences is no error; what does not
+    depend on them is still looked at."""
+    none = dict(B=0, q_start=None, ctx_len=None, page_table=None, max_new=0)
+    for b in (batch(), batch(**none)):
+        assert append(L, b=b, T=0, qkv=None, qo=None, pos=None) == OK
+        assert attend(L, b=b, T=0, q=None, out=None) == OK
+        assert attend(L, b=b, T=0, q=None, out=None, mask=None, words=1) == OK
+    assert compact(L, b=batch(**none), acc=None, n=None) == OK
+    assert logprobs(L, T=0, x=None, targets=None, lp=None, ids=None, top=None) == OK
+    assert logprobs(L, T=0, x=None, targets=None, lp=None, ids=None, top=None, n=0) == OK
+    assert append(L, T=0, qkv=None, qo=None, pos=None, cs=None) == BAD
+    assert append(L, T=0, qkv=None, qo=None, pos=None, rot=6) == UNSUP
+    assert attend(L, T=0, q=None, out=None, ws=None) == BAD
+    assert attend(L, T=0, q=None, out=None, n=10) == WS
+    assert attend(L, T=4, mask=None, words=1) == BAD
+    assert compact(L, b=batch(**none), acc=None, n=None, most=0) == BAD
+    assert logprobs(L, T=0, x=None, targets=None, lp=None, ids=None, top=None, V=0) == BAD
+
+
 def test_python_binding_refuses_tensors_that_do_not_fit():
     k = torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16)
     c = m.make_kv_cache(k, k.clone())
