@@ -109,7 +109,7 @@ moe_status moe_qk_norm_rope_append(const moe_kv_cache* cache, const moe_kv_batch
     if (rc != MOE_OK) return rc;
     if (T < 0 || !(eps >= 0.f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
     if (T > kMaxT) return MOE_ERR_UNSUPPORTED;
-    if (!at16(qkv) || !at16(q_out) || !at16(q_norm_w) || !at16(k_norm_w)) return MOE_ERR_INVALID_ARG;
+    if (!at16(qkv) || !at16(q_out) || !at16(q_norm_w) || !at16(k_norm_w) || !at4(bad_tokens)) return MOE_ERR_INVALID_ARG;
     const int64_t d = cache->head_dim;
     if (!row_ok(qkv_stride, (n_q + 2 * cache->n_kv) * d) || !row_ok(q_stride, n_q * d)) return MOE_ERR_INVALID_ARG;
     if (!qk_norm_rope_supported(cache->head_dim, rot_dim)) return MOE_ERR_UNSUPPORTED;
@@ -192,7 +192,7 @@ moe_status moe_kv_compact(const moe_kv_cache* cache, const moe_kv_batch* batch, 
     moe_status rc = check_cache(cache);
     if (rc == MOE_OK) rc = check_batch(batch);
     if (rc != MOE_OK) return rc;
-    if (n_layers < 1 || max_accept < 1 || !at4(accepted) || !at4(n_accepted)) return MOE_ERR_INVALID_ARG;
+    if (n_layers < 1 || max_accept < 1 || !at4(accepted) || !at4(n_accepted) || !at4(bad_seqs)) return MOE_ERR_INVALID_ARG;
     if (n_layers > 4096 || max_accept > 1024) return MOE_ERR_UNSUPPORTED;
     const int esz = cache->dtype == MOE_BF16 ? 2 : 1;
     if (!stride_ok(layer_stride, n_layers, cache->head_dim, esz)) return MOE_ERR_INVALID_ARG;

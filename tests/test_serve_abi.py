@@ -134,6 +134,15 @@ def test_logprobs_refusals(L):
     assert logprobs(L, T=0) == OK
 
 
+def test_counters_have_to_be_aligned(L):
+    """The kernels add to them with 4-byte atomics, which an odd address would fault."""
+    for off in (1, 2, 3):
+        assert append(L, bad=FAKE + off) == BAD
+        assert compact(L, bad=FAKE + off) == BAD
+        assert append(L, bad=FAKE + off, b=batch(B=0)) == BAD and compact(L, bad=FAKE + off, b=batch(B=0)) == BAD
+    assert append(L, bad=FAKE + 4, b=batch(B=0)) == OK and compact(L, bad=FAKE + 4, b=batch(B=0)) == OK
+
+
 def test_arrays_without_elements_may_be_null(L):
     """An empty tensor's address is NULL: a step without rows or sequences is no error; what does not
     depend on them is still looked at."""
