@@ -397,6 +397,8 @@ def moe_token_logprobs(logits, targets, logprobs, entropy=None, top_ids=None, to
     tg = None if targets is None else _dense("targets", targets, torch.int32, (T,), dev)
     lp = None if logprobs is None else _dense("logprobs", logprobs, f32, (T,), dev)
     en = None if entropy is None else _dense("entropy", entropy, f32, (T,), dev)
+    if (top_ids is None) != (top_logprobs is None) or (top_ids is not None and top_ids.shape != top_logprobs.shape):
+        raise ValueError("top_ids and top_logprobs: both [T, n], or neither")
     n = 0 if top_ids is None else top_ids.shape[1]
     ids = top = None
     if n:

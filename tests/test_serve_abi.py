@@ -195,6 +195,15 @@ def test_python_binding_refuses_tensors_that_do_not_fit():
         m.moe_qk_norm_rope_append(c, b, 4, 64, 1e-5, q, i32(4), None, None, torch.zeros(10, 64), q)
 
 
+def test_alternatives_need_both_outputs():
+    """Ids without log probabilities, or the other way round, are refused, not left unwritten."""
+    ids, top = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3)
+    for kw in (dict(top_ids=ids), dict(top_logprobs=top), dict(top_ids=ids[:, :0], top_logprobs=top),
+               dict(top_ids=ids, top_logprobs=top[:, :2])):
+        with pytest.raises(ValueError, match="top"):
+            m.moe_token_logprobs(torch.zeros(2, 8), None, None, **kw)
+
+
 def test_layers_behind_the_allocation_are_refused():
     layers = torch.zeros(3, 4, 2, 16, 128, dtype=torch.bfloat16)
     more = torch.zeros(3, 4, 2, 16, 128, dtype=torch.bfloat16)
