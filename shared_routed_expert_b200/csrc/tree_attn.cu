@@ -17,8 +17,9 @@ std::atomic<int> g_stall{0};
 
 // Joins the items that a cut between two shares goes through: block x the one that begins
 // in share x and does not end there; a warp takes every 16th row. Bound by latency and L2
-// (some tens of MB), so it is launched early and waits on the device for the kernel before it
-// (13 of 187 us for trees of up to 61 nodes; 4-token chains with a block per 4 rows 113 us, per
+// (some tens of MB). Its launch is hidden behind the kernel before it, whose blocks have all ended
+// when it starts (none of them lets it start sooner) and whose results it waits for on the device
+// (13 of 185 us for trees of up to 61 nodes; 4-token chains with a block per 4 rows 113 us, per
 // 16 rows 108 us, with 8 parts' loads in flight instead of 4 109 us).
 template <int EPL>
 __global__ void __launch_bounds__(JN_WARPS * 32) join_kernel(const AttnArgs a, const int M, const Partials p) {

@@ -107,8 +107,9 @@ __device__ __forceinline__ void attend_row(const AttnArgs& a, int b, const SeqIn
 }
 
 // Whether one of the keys [lo, hi) that a row (token i of the sequence; -1: one that sees no new token) does
-// not see has a value with an infinity or NaN, a lane per key. If none has, a NaN in the row's result is its own, and there is nothing to
-// compute again (one NaN among 4000 cached values, seen by all rows, made calls 4 to 180 times as long).
+// not see has a value with an infinity or NaN, a lane per key. If none has, a NaN in the row's result is its
+// own, and there is nothing to compute again (one NaN among 4000 cached values, seen by all rows, made calls 4
+// to 180 times as long).
 template <int D, bool F8>
 __device__ __forceinline__ bool hides_infinities(const AttnArgs& a, int b, const SeqInfo& s, int i, int kv_head, int lo, int hi,
                                               int lane) {

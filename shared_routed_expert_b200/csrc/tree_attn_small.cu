@@ -13,8 +13,8 @@
 // per SM, with Q in shared memory to leave a thread within 128 registers, and no warp spent
 // on loads alone (two blocks of 4 warps and a loading warp, Q in registers: 158 us for 64
 // decode rows of 96 heads over 544 MB of E4M3 cache, here 120 us; 223 us for 128 rows over
-// 566 MB of bf16 cache). 64 decode rows of 96 heads of 128: bf16 6.1 TB/s (1.09 GB in 178 us),
-// E4M3 4.5 TB/s, bound by the chain of a chunk (conversions, two products, exponentials) in
+// 566 MB of bf16 cache). 64 decode rows of 96 heads of 128: bf16 6.1 TB/s (1.09 GB in 180 us),
+// E4M3 4.5 TB/s (4.3 back to back at the power limit), bound by the chain of a chunk (conversions, two products, exponentials) in
 // 16 warps (chunks of half as many keys: 152 us). Heads of 64: 5.9 TB/s, of 256: 6.0 TB/s.
 //   bf16 cache: Q, K, P, V as bf16.
 //   E4M3 cache: K and V codes convert to fp16 exactly; Q rows are scaled by a power of two
@@ -711,7 +711,8 @@ cudaError_t launch_d(const AttnArgs& a, void* partials, int sms, cudaStream_t st
 // tokens of 10 heads over 2 kv heads, E4M3, 14 us here, 28 us there; 2 sequences of 49 and 149 tokens of
 // 12 heads behind 1278 keys 24 and 39 us; 3 sequences of 266 to 800 tokens of 4 heads behind
 // 1515 keys, 10 units a block, 60 us and 41 us there. The contexts are on the device; what the
-// page table can hold bounds them.
+// page table can hold bounds them, so a table much wider than its sequences (131072 tokens: 515 units)
+// leaves no call but one of a tile or two short, and those drafts take the tiles' 28 us.
 bool tree_attn_short(const AttnArgs& a) {
     const long long tiles = (static_cast<long long>(a.T) * a.group / 32 + a.c.B) * a.c.n_kv;
     const long long units = (static_cast<long long>(a.c.max_pages) << a.c.page_shift) / 256 + 3;

@@ -15,15 +15,18 @@
 // Roles: warps 0-3 and 4-7 the two halves' softmax, loads of Q and epilogue; warp 8 issues
 // the products; warp 9 streams K and V boxes (one per page piece and 128-byte span) through
 // a ring in shared memory. Every wait is bounded.
-// Measured, 96 heads of 128 over 8 kv heads, bf16: a chunk of 4096 rows behind 12288 keys 2.77 ms,
-// 1040 TFLOP/s at the power limit of 1000 W (1.75 GHz); trees of 23 to 61 nodes of 12 sequences
-// 187 us (730 TFLOP/s; the join is 13 us of it); 4-token chains of 32 sequences 107 us, 5.3 TB/s.
+// Measured, 96 heads of 128 over 8 kv heads, bf16: a chunk of 4096 rows behind 12288 keys 2.72 to
+// 2.85 ms, 1010 to 1060 TFLOP/s at the power limit of 1000 W (1.7 to 1.78 GHz); trees of 23 to 61 nodes
+// of 12 sequences 185 us in short runs (740 TFLOP/s; the join is 13 us of it), 212 us back to back at
+// the power limit (640 TFLOP/s, 1.74 GHz); 4-token chains of 32 sequences 107 us (5.3 TB/s) and 120 us
+// (4.7 TB/s, 1.66 GHz).
 // The exponentials of a half take about as long as its products (128 per thread and step). No
 // faster for the chunk: the whole row of S in registers (2987 us, spills), a quartic in place of
 // 1/8 to 3/8 of the exponentials (3004 to 3137 us), P in two arrivals (2909 us, one 2913 then),
 // steps of 64 keys with two S (4950 us: a product of N = 64 takes as long as one of 128).
 // E4M3 caches: the boxes go to a ring of codes, from which warps 10 and 11 write K and V as
-// fp16 (exact) to the products' ring (2048 rows behind 8192 keys: 1088 us, bf16 910 us). Q rows are scaled by a power of two to fp16 (exact for
+// fp16 (exact) to the products' ring (2048 rows behind 8192 keys: 1110 us, bf16 870 to 940 us; the
+// 4-token chains 175 us, the trees 256 us). Q rows are scaled by a power of two to fp16 (exact for
 // everything within 2^-28 of the row's largest entry) and P is fp16, raised by 2^7 (kLift). (E4M3
 // operands would need P in 4 significant bits.)
 #include "kernels.cuh"

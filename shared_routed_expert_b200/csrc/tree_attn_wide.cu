@@ -11,8 +11,8 @@
 // rescaled after the product in front has finished. 128 exponentials per thread and step stand
 // against four products of 128 x 128 x 128, as there; with 192 threads a row of S stays in registers.
 // Measured, 16 heads over 4 kv heads, bf16: 4096 rows behind 4096 keys 408 us, 1010 TFLOP/s (the 16-row
-// products of tree_attn_small.cu: 1944 us), 1024 rows behind 2048 keys 75 us; E4M3 108 us, bound by
-// the conversion (two warps instead of four: 130 us).
+// products of tree_attn_small.cu: 1944 us), 1024 rows behind 2048 keys 75 us; E4M3 108 to 120 us, bound
+// by the conversion (two warps instead of four: 130 us).
 // Roles: warps 0-3 softmax, loads of Q and epilogue; warp 4 the products; warp 5 streams K and V;
 // E4M3: warps 6 to 9 convert codes to fp16. Every wait is bounded.
 #include "kernels.cuh"
