@@ -57,6 +57,11 @@ bool tree_attn_take_stall() {
     return false;
 }
 
+long long tile_wait_limit(const AttnArgs& a) {
+    const long long keys = static_cast<long long>(a.c.max_pages) << a.c.page_shift, most = 1ll << 22;
+    return (16ll << 30) + (keys < most ? keys : most) * 32 * 8192;
+}
+
 // K or V of a cache as (dimension within a 128-byte span, slot, span, kv head, page): a box
 // is one span of box_rows slots of one head, stored [slot][128 bytes] (64 for 64-byte
 // rows) with the swizzle of that width.

@@ -521,6 +521,10 @@ cudaError_t launch_tree_attn_join(const AttnArgs& a, int M, Partials p, int bloc
 // where the partial results of up to `blocks` blocks with tiles of M rows lie in memory
 Partials partials_at(void* mem, int blocks, int M);
 size_t partials_bytes(int blocks, int M, int head_dim);
+// Cycles after which a wait of the tile kernels gives up: 9 s, and what a warp may spend on computing 32 rows
+// again behind as many keys as the page table holds (8192 cycles a row and key; 1200 were measured where they
+// come from L2, heads of 256), while the others wait for it
+long long tile_wait_limit(const AttnArgs& a);
 bool make_kv_map(CUtensorMap* m, const AttnArgs& a, bool v, int box_rows);
 // testing hook: the next n calls run with loads that are never issued and a ~10 ms wait limit
 void tree_attn_inject_stall(int n_calls);

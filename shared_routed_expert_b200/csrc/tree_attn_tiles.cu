@@ -692,7 +692,7 @@ cudaError_t launch_tiles(const AttnArgs& a, void* partials, int sms, cudaStream_
     const int box = page < TK ? page : TK;
     p.box_shift = page < TK ? a.c.page_shift : 7;
     p.stall = tree_attn_take_stall();
-    p.wait_limit = p.stall ? 20ll << 20 : 16ll << 30;
+    p.wait_limit = p.stall ? 20ll << 20 : tile_wait_limit(a);
     if (!make_kv_map(&p.tk, a, false, box) || !make_kv_map(&p.tv, a, true, box)) return cudaErrorInvalidValue;
     const int blocks = sms < kTileBlocks ? sms : kTileBlocks;
     p.part = partials_at(partials, blocks, kTileRows);

@@ -125,3 +125,40 @@ def test_cached_and_unseen_values_without_a_number(n, ctx, n_q, n_kv, d, tree, k
     over = q.clone()
     m.moe_tree_attention(cache, batch, n_q, over, over, ws, tree_mask=mask_tensor(sets, 2) if tree else None)
     assert torch.equal(over.view(torch.int16), out.view(torch.int16))
+
+
+def test_rows_that_are_computed_again_behind_a_long_context():
+    """A drafted token's NaN behind 524288 cached keys: the rows that do not see it take the warps that compute
+    them again 10 s; the other warps wait for them, and the call ends well. (All cached pages are one
+    page; as many sequences as blocks, so that the rows' keys are in one block's share.)"""
+    B, n, n_q, d, page, ctx = 150, 32, 4, 256, 256, 524288
+    i32 = dict(dtype=torch.int32, device=DEV)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(43)
+    k = torch.randn(B + 1, 1, page, d, generator=g, device=DEV).to(torch.bfloat16)
+    v = torch.randn(B + 1, 1, page, d, generator=g, device=DEV).to(torch.bfloat16)
+    v[1, 0, 5, 3] = math.nan                                # sequence 0, new token 5
+    table = torch.zeros(B, ctx // page + 1, **i32)
+    table[:, -1] = torch.arange(1, B + 1, **i32)
+    cache = m.make_kv_cache(k, v)
+    batch = m.make_kv_batch(torch.arange(B + 1, **i32) * n, torch.full((B,), ctx, **i32), table, n)
+    q = torch.randn(B * n, n_q * d, generator=g, device=DEV).to(torch.bfloat16)
+    out, ws = torch.empty_like(q), m.alloc_tree_attention_workspace(cache, n_q, B * n)
+    mask = torch.tensor([[1 << i] for i in range(n)], dtype=torch.int64, device=DEV).repeat(B, 1)
+    m.moe_tree_attention(cache, batch, n_q, q, out, ws, tree_mask=mask)       # (a token sees the cached ones and itself)
+    assert m.moe_get_status(ws) == _lib.MOE_OK
+    got = out.view(B, n, n_q, d).double()
+    # each key of the page counts ctx / page times
+    K, V = k[0, 0].double(), torch.nan_to_num(v[0, 0].double())
+    for b in (0, 1, B - 1):
+        for t in (0, 4, 6, n - 1):
+            x = q.view(B, n, n_q, d)[b, t].double() @ torch.cat([K, k[b + 1, 0, t:t + 1].double()]).T / math.sqrt(d)
+            w = torch.cat([torch.full((page,), ctx / page, device=DEV), torch.ones(1, device=DEV)]).double()
+            p = w * torch.exp(x - x.amax(1, keepdim=True))
+            p = p / p.sum(1, keepdim=True)
+            vals = torch.cat([V, v[b + 1, 0, t:t + 1].double()])
+            e = (d + 4) * 2.0 ** -24 / math.sqrt(d) * (q.view(B, n, n_q, d)[b, t].double().abs() @ K.abs().T).amax(1)
+            # the roundings of attention_ref, and 2^-24 for each of a lane's additions in a row
+            tol = 2.0 ** -8 * (p @ vals).abs() + (2.0 ** -8 + 4 * e + 2.0 ** -18 + (ctx + n) * 2.0 ** -24)[:, None] * (p @ vals.abs())
+            assert bool(((got[b, t] - p @ vals).abs() <= tol).all()), (b, t)
+    assert bool(torch.isnan(got[0, 5, :, 3]).all()) and int(torch.isnan(got).sum()) == n_q
